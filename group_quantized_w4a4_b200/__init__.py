@@ -33,7 +33,26 @@ __all__ = [
     "apex_set_wait_limit_ns", "apex_status_string", "apex_debug_withhold_step",
     "apex_debug_trace_next_gemm", "apex_debug_gemm_plan", "apex_debug_partials_split",
     "pack_weights", "quantize_act", "gemm", "workspace",
+    "apex_quantize_act_fp8_block", "apex_pack_weights_fp8_block", "apex_gemm_fp8_block",
+    "apex_linear_fp8_block", "apex_linear_fp8_block_workspace_size", "apex_route_experts",
+    "apex_plan_experts", "apex_moe_mlp_fp8_block", "apex_moe_mlp_fp8_block_workspace_size",
+    "apex_block_norm", "quantize_act_fp8_block", "pack_weights_fp8_block", "gemm_fp8_block",
+    "linear_fp8_block", "route_experts", "plan_experts", "moe_mlp_fp8_block", "block_norm",
 ]
+
+# The block-scaled FP8, expert and block-norm functions live in fp8_block.py, which needs torch
+# at import; they are resolved on first use, as the rest of this module needs torch only in calls.
+_FP8_BLOCK = frozenset(n for n in __all__ if n.endswith(("_fp8_block", "_fp8_block_workspace_size",
+                                                         "_experts", "block_norm")))
+
+
+def __getattr__(name):
+    if name in _FP8_BLOCK:
+        from . import fp8_block
+        value = globals()[name] = getattr(fp8_block, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 APEX_OK = 0
 APEX_ERR_INVALID_ARG = 1
@@ -139,6 +158,8 @@ def load_library(build_if_missing: bool = True):
         lib.apex_debug_trace_next_gemm.restype = None
         lib.apex_debug_gemm_plan.argtypes = [I64, I64, I64, I32, I32, P]
         lib.apex_debug_gemm_plan.restype = st
+        from . import fp8_block as _fb
+        _fb.declare(lib)
         _lib = lib
         return lib
 

@@ -9,13 +9,18 @@
 #include <string.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "apex_w4a4.h"
+#include "block_norm.cuh"
 #include "dual.cuh"
+#include "f8_block.cuh"
 #include "gemm.cuh"
 #include "gemm_f8.cuh"
+#include "gemm_f8_block.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
+#include "route.cuh"
 
 namespace {
 
@@ -1025,3 +1030,7 @@ apex_status_t apex_w4a4_gemm_fp8_dual(int64_t M, int64_t N, int64_t K, int32_t g
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- block-scaled FP8, experts, norms
+
+#include "fp8_block_host.cuh"

@@ -1,0 +1,159 @@
+// block_norm.cuh -- what stands between two blocks of a model, in one pass over a token:
+//
+//   z = x                                                     (the block's output)
+//   z = z * rsqrt(mean(z^2) + eps) * (off + post_weight)      (optional: norm behind the block)
+//   z = z * gate                                              (optional)
+//   h = residual + alpha * z                                  (the new residual stream)
+//   y = h * rsqrt(mean(h^2) + eps) * (off + pre_weight)       (optional: norm before the next)
+//
+// with h and y stored in x's type, and y also as the next product's block-scaled E4M3 operand
+// (f8_block.cuh).  Everything between is fp32: h is rounded where it is stored, y and its codes
+// are formed from the unrounded values.  The combine of the experts' products is here too: a
+// weighted sum over a token's choices.
+#pragma once
+#include <stdint.h>
+
+#include "f8_block.cuh"
+#include "ptx.cuh"
+
+namespace apex {
+
+struct NormArgs {
+  const void *x, *residual, *post, *gate, *pre;   // all but x may be null
+  int T, H, G;             // G = ceil(H / 128)
+  int rows_per_gate;       // row t takes gate row t / rows_per_gate
+  float alpha, eps, off;
+  void *h, *y;             // may be null
+  uint8_t* codes;          // may be null
+  float* scales;
+};
+
+// Sum over the CTA; every thread gets it.  One slot array per call site.
+__device__ __forceinline__ float block_sum(float v, float* s_part, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = (threadIdx.x & 31) < warps ? s_part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+// One CTA per token; thread i holds chunks i, i + blockDim, ... of 8 elements in registers, so
+// every tensor is read and written once.
+template <int DT, int NC>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a) {
+  using D = DTraits<DT>;
+  __shared__ float s_part[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warps = blockDim.x >> 5;
+  const size_t base = (size_t)blockIdx.x * a.H;
+  float z[NC][8];
+  bool in[NC];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (threadIdx.x + i * blockDim.x) * 8;
+    in[i] = c < a.H;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[i][j] = 0.0f;
+    if (in[i]) load8<DT>(a.x, base + c, z[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(z[i][j], z[i][j], ss);
+  }
+  float rs = 1.0f;
+  if (a.post) rs = __frsqrt_rn(block_sum(ss, s_part[0], warps) / (float)a.H + a.eps);
+  const size_t gbase = a.gate ? (size_t)(blockIdx.x / a.rows_per_gate) * a.H : 0;
+  ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (threadIdx.x + i * blockDim.x) * 8;
+    if (!in[i]) continue;
+    if (a.post) {
+      float w[8];
+      load8<DT>(a.post, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * rs * (a.off + w[j]);
+    }
+    if (a.gate) {
+      float w[8];
+      load8<DT>(a.gate, gbase + c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] *= w[j];
+    }
+    if (a.residual) {
+      float w[8];
+      load8<DT>(a.residual, base + c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = fmaf(a.alpha, z[i][j], w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] *= a.alpha;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(z[i][j], z[i][j], ss);
+    if (a.h)
+      *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.h) + base + c) =
+          make_uint4(D::pack(z[i][0], z[i][1]), D::pack(z[i][2], z[i][3]),
+                     D::pack(z[i][4], z[i][5]), D::pack(z[i][6], z[i][7]));
+  }
+  if (!a.pre) return;
+  rs = __frsqrt_rn(block_sum(ss, s_part[1], warps) / (float)a.H + a.eps);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (threadIdx.x + i * blockDim.x) * 8;
+    if (in[i]) {
+      float w[8];
+      load8<DT>(a.pre, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * rs * (a.off + w[j]);
+      if (a.y)
+        *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.y) + base + c) =
+            make_uint4(D::pack(z[i][0], z[i][1]), D::pack(z[i][2], z[i][3]),
+                       D::pack(z[i][4], z[i][5]), D::pack(z[i][6], z[i][7]));
+    }
+    if (a.codes) {   // 16 lanes hold one group (the shuffles are warp-wide)
+      const F8Scale q = f8_scale(half_warp_max(absmax8_bits(z[i])));
+      if (in[i]) {
+        *reinterpret_cast<uint2*>(a.codes + base + c) = f8_codes8(z[i], q);
+        if ((threadIdx.x & 15) == 0) a.scales[(size_t)blockIdx.x * a.G + c / 128] = q.s;
+      }
+    }
+  }
+}
+
+// out[t] = sum_j weights[t,j] * y[t * k + j] over the choices with an id in [0, E), in the
+// order of j, in fp32.
+template <int DT>
+__global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y,
+                                                      const float* __restrict__ weights,
+                                                      const int32_t* __restrict__ ids, int T, int H,
+                                                      int k, int E, void* __restrict__ out) {
+  using D = DTraits<DT>;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int chunks = H / 8;
+  const long long n = (long long)T * chunks;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n;
+       i += (long long)gridDim.x * 256) {
+    const long long t = i / chunks;
+    const int c = (int)(i - t * chunks) * 8;
+    float acc[8] = {};
+    for (int j = 0; j < k; ++j) {
+      const int id = __ldg(ids + t * k + j);
+      if (id < 0 || id >= E) continue;
+      const float w = __ldg(weights + t * k + j);
+      float v[8];
+      load8<DT>(y, (size_t)(t * k + j) * H + c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+    *reinterpret_cast<uint4*>(static_cast<typename D::T*>(out) + (size_t)t * H + c) =
+        make_uint4(D::pack(acc[0], acc[1]), D::pack(acc[2], acc[3]), D::pack(acc[4], acc[5]),
+                   D::pack(acc[6], acc[7]));
+  }
+}
+
+}  // namespace apex

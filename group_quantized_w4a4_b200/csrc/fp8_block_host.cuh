@@ -1,0 +1,419 @@
+// fp8_block_host.cuh -- host side of the block-scaled FP8, expert and block-norm entry points:
+// argument checks, tensor maps, launches.  Included by apex_w4a4.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+using apex::FBArgs;
+using apex::FBCfg;
+
+bool is_16bit(int32_t dt) { return dt == APEX_DTYPE_F16 || dt == APEX_DTYPE_BF16; }
+bool is_float(int32_t dt) { return is_16bit(dt) || dt == APEX_DTYPE_F32; }
+size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxBlockDim = 1 << 20;   // largest N, K, H of these entry points
+constexpr int64_t kMaxSlots = 1 << 30;
+
+apex_status_t launched(cudaError_t e) {
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();   // reported here, not by the caller's next call
+    return APEX_ERR_CUDA;
+  }
+  return APEX_OK;
+}
+
+// 3-D map over E4M3 codes [Z][rows][K]; box = 128 codes x box_rows rows of one matrix, 128-byte
+// swizzle; rows and columns outside a matrix read as zeros.
+bool make_codes3_map(CUtensorMap* map, const void* base, int64_t Z, int64_t rows, int64_t K,
+                     int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)Z};
+  cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)(K * rows)};
+  cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+template <typename F>
+cudaError_t set_smem(F kern, int bytes, int* attr_dev) {   // once per device and kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (*attr_dev != dev) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) *attr_dev = dev;
+  }
+  return e;
+}
+
+template <int BN, int KIND, int DT>
+apex_status_t launch_fb(const CUtensorMap& ma, const CUtensorMap& mb, FBArgs a, cudaStream_t s) {
+  using C = FBCfg<BN>;
+  auto kern = apex::f8_block_gemm_kernel<BN, KIND, DT>;
+  static thread_local int attr_dev = -1;
+  if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
+  return launched(launch_pdl(kern, (unsigned)a.P, C::THREADS, (size_t)C::SMEM, s, ma, mb, a));
+}
+
+template <int DT>
+cudaError_t f8_quantize_t(const void* x, int64_t M, int64_t K, void* codes, void* scales,
+                          cudaStream_t s) {
+  const int G = (int)ceil_div(K, 128);
+  const int g_shift = (G & (G - 1)) == 0 ? __builtin_ctz((unsigned)G) : -1;
+  const int64_t units = M * G;
+  const bool many = units >= kQuantBatchMinUnits;
+  const int64_t per_block = 8 * (many ? 2 : 1);
+  int64_t blocks = ceil_div(units, per_block);
+  const int64_t cap = (int64_t)dev_info().sms * 32;
+  if (blocks > cap) blocks = cap;
+  return many ? launch_pdl(apex::f8_quantize_act_kernel<DT, 2>, (unsigned)blocks, 128, 0, s, x,
+                           (int)M, (int)K, G, g_shift, static_cast<uint8_t*>(codes),
+                           static_cast<float*>(scales))
+              : launch_pdl(apex::f8_quantize_act_kernel<DT, 1>, (unsigned)blocks, 128, 0, s, x,
+                           (int)M, (int)K, G, g_shift, static_cast<uint8_t*>(codes),
+                           static_cast<float*>(scales));
+}
+
+apex_status_t check_f8_dims(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || K % 16) return APEX_ERR_INVALID_ARG;
+  if (M > kMaxSlots || N > kMaxBlockDim || K > kMaxBlockDim) return APEX_ERR_UNSUPPORTED;
+  if (M * ceil_div(K, 128) >= (1ll << 31)) return APEX_ERR_UNSUPPORTED;
+  return APEX_OK;
+}
+
+FBArgs fb_args(int64_t M, int64_t N, int64_t K, const void* sa, const void* sw) {
+  FBArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.G = (int)ceil_div(K, 128);
+  a.NB = (int)ceil_div(N, 128);
+  a.sa = static_cast<const float*>(sa);
+  a.sw = static_cast<const float*>(sw);
+  a.s_vec = a.G % 4 == 0 && aligned(sa, 16) && aligned(sw, 16);
+  a.wait_ns = g_wait_limit_ns;
+  return a;
+}
+
+apex_status_t fb_dense(int64_t M, int64_t N, int64_t K, const void* a_codes, const void* a_scales,
+                       const void* w_codes, const void* w_scales, int32_t dtype, void* y,
+                       cudaStream_t s) {
+  FBArgs a = fb_args(M, N, K, a_scales, w_scales);
+  a.y = y;
+  a.y_vec = N % 8 == 0 && aligned(y, 16);
+  a.tiles_m = (int)ceil_div(M, 128);
+  const int sms = dev_info().sms;
+  const bool wide = (int64_t)a.tiles_m * ceil_div(N, 256) >= sms;
+  a.tiles_n = (int)ceil_div(N, wide ? 256 : 128);
+  const int64_t T = (int64_t)a.tiles_m * a.tiles_n;
+  if (T >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
+  a.P = (int)(T < sms ? T : sms);
+  CUtensorMap ma, mb;
+  if (!make_expanded_map(&ma, a_codes, M, K, 128) || !make_codes3_map(&mb, w_codes, 1, N, K, 128))
+    return APEX_ERR_CUDA;
+  if (dtype == APEX_DTYPE_F16)
+    return wide ? launch_fb<256, apex::FB_DENSE, apex::DT_F16>(ma, mb, a, s)
+                : launch_fb<128, apex::FB_DENSE, apex::DT_F16>(ma, mb, a, s);
+  return wide ? launch_fb<256, apex::FB_DENSE, apex::DT_BF16>(ma, mb, a, s)
+              : launch_fb<128, apex::FB_DENSE, apex::DT_BF16>(ma, mb, a, s);
+}
+
+struct MoeWork {   // byte offsets into the workspace of apex_moe_mlp_fp8_block
+  size_t xq, xs, hq, hs, y, total;
+};
+MoeWork moe_work(int64_t T, int64_t k, int64_t H, int64_t I) {
+  MoeWork w;
+  const size_t S = (size_t)T * (size_t)k;
+  w.xq = 0;
+  w.xs = w.xq + pad256((size_t)T * H);
+  w.hq = w.xs + pad256((size_t)T * ceil_div(H, 128) * 4);
+  w.hs = w.hq + pad256(S * I);
+  w.y = w.hs + pad256(S * ceil_div(I, 128) * 4);
+  w.total = w.y + pad256(S * H * 2);
+  return w;
+}
+
+apex_status_t check_moe(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
+  if (T <= 0 || E <= 0 || k <= 0 || H <= 0 || I <= 0 || H % 16 || I % 16)
+    return APEX_ERR_INVALID_ARG;
+  if (E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || H > kMaxBlockDim || I > kMaxBlockDim ||
+      T > kMaxSlots)
+    return APEX_ERR_UNSUPPORTED;
+  if (T * k >= kMaxSlots || T * k * ceil_div(H > I ? H : I, 128) >= (1ll << 31))
+    return APEX_ERR_UNSUPPORTED;
+  return APEX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+apex_status_t apex_quantize_act_fp8_block(const void* x, int32_t dtype, int64_t M, int64_t K,
+                                          void* codes, void* scales_f32, void* stream) {
+  if (!x || !codes || !scales_f32) return APEX_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return APEX_ERR_UNSUPPORTED;
+  apex_status_t st = check_f8_dims(M, 1, K);
+  if (st != APEX_OK) return st;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales_f32, 4)) return APEX_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launched(dtype == APEX_DTYPE_F16
+                      ? f8_quantize_t<apex::DT_F16>(x, M, K, codes, scales_f32, s)
+                      : f8_quantize_t<apex::DT_BF16>(x, M, K, codes, scales_f32, s));
+}
+
+apex_status_t apex_pack_weights_fp8_block(const void* w, int32_t dtype, int64_t E, int64_t N,
+                                          int64_t K, void* codes, void* scales_f32, void* stream) {
+  if (!w || !codes || !scales_f32 || E <= 0) return APEX_ERR_INVALID_ARG;
+  if (!is_float(dtype)) return APEX_ERR_UNSUPPORTED;
+  apex_status_t st = check_f8_dims(1, N, K);
+  if (st != APEX_OK) return st;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales_f32, 4)) return APEX_ERR_ALIGNMENT;
+  const int G = (int)ceil_div(K, 128), NB = (int)ceil_div(N, 128);
+  if (E > (1ll << 20) || (int64_t)G * NB * E >= (1ll << 31)) return APEX_ERR_UNSUPPORTED;
+  const unsigned blocks = (unsigned)((int64_t)G * NB * E);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto kern) {
+    return launched(launch_pdl(kern, blocks, 256, 0, s, w, (int)N, (int)K, G, NB,
+                               static_cast<uint8_t*>(codes), static_cast<float*>(scales_f32)));
+  };
+  if (dtype == APEX_DTYPE_F16) return run(apex::f8_pack_weights_kernel<apex::DT_F16>);
+  if (dtype == APEX_DTYPE_BF16) return run(apex::f8_pack_weights_kernel<apex::DT_BF16>);
+  return run(apex::f8_pack_weights_kernel<apex::DT_F32>);
+}
+
+apex_status_t apex_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* a_codes,
+                                  const void* a_scales, const void* w_codes, const void* w_scales,
+                                  int32_t dtype, void* y, void* stream) {
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !y) return APEX_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return APEX_ERR_UNSUPPORTED;
+  apex_status_t st = check_f8_dims(M, N, K);
+  if (st != APEX_OK) return st;
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(a_scales, 4) ||
+      !aligned(w_scales, 4) || !aligned(y, 2))
+    return APEX_ERR_ALIGNMENT;
+  return fb_dense(M, N, K, a_codes, a_scales, w_codes, w_scales, dtype, y,
+                  static_cast<cudaStream_t>(stream));
+}
+
+size_t apex_linear_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_f8_dims(M, N, K) != APEX_OK) return 0;
+  return pad256((size_t)M * K) + pad256((size_t)M * ceil_div(K, 128) * 4);
+}
+
+apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void* x, int32_t dtype,
+                                    const void* w_codes, const void* w_scales, void* y,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !w_codes || !w_scales || !y || !workspace) return APEX_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return APEX_ERR_UNSUPPORTED;
+  apex_status_t st = check_f8_dims(M, N, K);
+  if (st != APEX_OK) return st;
+  if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 2) ||
+      !aligned(workspace, 256))
+    return APEX_ERR_ALIGNMENT;
+  if (workspace_bytes < apex_linear_fp8_block_workspace_size(M, N, K)) return APEX_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* sc = ws + pad256((size_t)M * K);
+  st = apex_quantize_act_fp8_block(x, dtype, M, K, ws, sc, stream);
+  if (st != APEX_OK) return st;
+  return fb_dense(M, N, K, ws, sc, w_codes, w_scales, dtype, y, static_cast<cudaStream_t>(stream));
+}
+
+apex_status_t apex_route_experts(const void* logits, int32_t dtype, int64_t T, int32_t E,
+                                 int32_t k, int32_t score, const void* bias_f32, int32_t groups,
+                                 int32_t topk_groups, int32_t renormalize, float scale,
+                                 const void* mask_u8, void* weights_f32, void* ids_i32,
+                                 void* stream) {
+  if (!logits || !weights_f32 || !ids_i32 || T <= 0 || E <= 0 || k <= 0 || groups <= 0 ||
+      topk_groups <= 0 || topk_groups > groups || E % groups)
+    return APEX_ERR_INVALID_ARG;
+  if (score != APEX_SCORE_SOFTMAX && score != APEX_SCORE_SIGMOID) return APEX_ERR_INVALID_ARG;
+  if (k > topk_groups * (E / groups)) return APEX_ERR_INVALID_ARG;
+  if (!is_float(dtype) || E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || groups > 32 ||
+      T * (int64_t)k >= kMaxSlots)
+    return APEX_ERR_UNSUPPORTED;
+  if (!aligned(logits, dtype == APEX_DTYPE_F32 ? 4 : 2) || !aligned(bias_f32, 4) ||
+      !aligned(weights_f32, 4) || !aligned(ids_i32, 4))
+    return APEX_ERR_ALIGNMENT;
+  apex::RouteArgs a;
+  a.logits = logits;
+  a.bias = static_cast<const float*>(bias_f32);
+  a.mask = static_cast<const uint8_t*>(mask_u8);
+  a.T = (int)T;
+  a.E = E;
+  a.k = k;
+  a.G = groups;
+  a.TG = topk_groups;
+  a.sigmoid = score == APEX_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.ids = static_cast<int32_t*>(ids_i32);
+  a.weights = static_cast<float*>(weights_f32);
+  int64_t blocks = ceil_div(T, apex::kRouteWarps);
+  const int64_t cap = (int64_t)dev_info().sms * 16;
+  if (blocks > cap) blocks = cap;
+  const size_t smem = groups > 1 ? (size_t)apex::kRouteWarps * E * 8 : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto kern) {
+    return launched(launch_pdl(kern, (unsigned)blocks, 32 * apex::kRouteWarps, smem, s, a));
+  };
+  auto by_width = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (E <= 64) return run(apex::route_kernel<DT, 2>);
+    if (E <= 128) return run(apex::route_kernel<DT, 4>);
+    if (E <= 256) return run(apex::route_kernel<DT, 8>);
+    return run(apex::route_kernel<DT, 16>);
+  };
+  if (dtype == APEX_DTYPE_F16) return by_width(std::integral_constant<int, apex::DT_F16>{});
+  if (dtype == APEX_DTYPE_BF16) return by_width(std::integral_constant<int, apex::DT_BF16>{});
+  return by_width(std::integral_constant<int, apex::DT_F32>{});
+}
+
+apex_status_t apex_plan_experts(const void* ids_i32, int64_t T, int32_t k, int32_t E,
+                                void* offsets_i32, void* order_i32, void* stream) {
+  if (!ids_i32 || !offsets_i32 || !order_i32 || T <= 0 || k <= 0 || E <= 0)
+    return APEX_ERR_INVALID_ARG;
+  if (E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || T >= kMaxSlots || T * (int64_t)k >= kMaxSlots)
+    return APEX_ERR_UNSUPPORTED;
+  if (!aligned(ids_i32, 4) || !aligned(offsets_i32, 4) || !aligned(order_i32, 4))
+    return APEX_ERR_ALIGNMENT;
+  return launched(launch_pdl(apex::plan_kernel, (unsigned)(E + 1), 256, 0,
+                             static_cast<cudaStream_t>(stream),
+                             static_cast<const int32_t*>(ids_i32), (int)(T * k), (int)E,
+                             static_cast<int32_t*>(offsets_i32),
+                             static_cast<int32_t*>(order_i32)));
+}
+
+size_t apex_moe_mlp_fp8_block_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H,
+                                             int64_t I) {
+  if (check_moe(T, E, k, H, I) != APEX_OK) return 0;
+  return moe_work(T, k, H, I).total;
+}
+
+apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                                     const void* x, int32_t dtype, const void* weights_f32,
+                                     const void* ids_i32, const void* offsets_i32,
+                                     const void* order_i32, const void* w13_codes,
+                                     const void* w13_scales, const void* w2_codes,
+                                     const void* w2_scales, void* y, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!x || !weights_f32 || !ids_i32 || !offsets_i32 || !order_i32 || !w13_codes || !w13_scales ||
+      !w2_codes || !w2_scales || !y || !workspace)
+    return APEX_ERR_INVALID_ARG;
+  if (!is_16bit(dtype)) return APEX_ERR_UNSUPPORTED;
+  apex_status_t st = check_moe(T, E, k, H, I);
+  if (st != APEX_OK) return st;
+  if (!aligned(x, 16) || !aligned(w13_codes, 16) || !aligned(w2_codes, 16) || !aligned(y, 16) ||
+      !aligned(workspace, 256) || !aligned(weights_f32, 4) || !aligned(ids_i32, 4) ||
+      !aligned(offsets_i32, 4) || !aligned(order_i32, 4) || !aligned(w13_scales, 4) ||
+      !aligned(w2_scales, 4))
+    return APEX_ERR_ALIGNMENT;
+  const MoeWork w = moe_work(T, k, H, I);
+  if (workspace_bytes < w.total) return APEX_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = apex_quantize_act_fp8_block(x, dtype, T, H, ws + w.xq, ws + w.xs, stream);
+  if (st != APEX_OK) return st;
+
+  const int64_t S = T * k;
+  const int sms = dev_info().sms;
+  // at most: one partly filled tile for each expert that has rows, and the full ones
+  const int64_t most_tiles = (S < E ? S : (int64_t)E) + S / 128;
+  auto with_experts = [&](FBArgs a, int64_t tiles_n) {
+    a.E = E;
+    a.slots = (int)S;
+    a.top_k = k;
+    a.offsets = static_cast<const int32_t*>(offsets_i32);
+    a.order = static_cast<const int32_t*>(order_i32);
+    a.tiles_n = (int)tiles_n;
+    const int64_t tiles = most_tiles * tiles_n;
+    a.P = (int)(tiles < sms ? tiles : sms);
+    return a;
+  };
+  if (most_tiles * ceil_div(H > I ? H : I, 128) >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
+
+  CUtensorMap mx, mw13, mh, mw2;
+  if (!make_expanded_map(&mx, ws + w.xq, T, H, 1) ||
+      !make_codes3_map(&mw13, w13_codes, 2 * (int64_t)E, I, H, 128) ||
+      !make_expanded_map(&mh, ws + w.hq, S, I, 128) ||
+      !make_codes3_map(&mw2, w2_codes, E, H, I, 128))
+    return APEX_ERR_CUDA;
+
+  FBArgs up = with_experts(fb_args(T, I, H, ws + w.xs, w13_scales), ceil_div(I, 128));
+  up.hq = ws + w.hq;
+  up.hs = reinterpret_cast<float*>(ws + w.hs);
+  st = launch_fb<256, apex::FB_UP, apex::DT_BF16>(mx, mw13, up, s);
+  if (st != APEX_OK) return st;
+
+  FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales), ceil_div(H, 256));
+  down.y = ws + w.y;
+  down.y_vec = 1;
+  const bool f16 = dtype == APEX_DTYPE_F16;
+  st = f16 ? launch_fb<256, apex::FB_DOWN, apex::DT_F16>(mh, mw2, down, s)
+           : launch_fb<256, apex::FB_DOWN, apex::DT_BF16>(mh, mw2, down, s);
+  if (st != APEX_OK) return st;
+
+  const unsigned blocks = grid_for(T * (H / 8), 256, 16);
+  return launched(f16 ? launch_pdl(apex::combine_kernel<apex::DT_F16>, blocks, 256, 0, s,
+                                   (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
+                                   static_cast<const int32_t*>(ids_i32), (int)T, (int)H, (int)k,
+                                   (int)E, y)
+                      : launch_pdl(apex::combine_kernel<apex::DT_BF16>, blocks, 256, 0, s,
+                                   (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
+                                   static_cast<const int32_t*>(ids_i32), (int)T, (int)H, (int)k,
+                                   (int)E, y));
+}
+
+apex_status_t apex_block_norm(const void* x, int32_t dtype, int64_t T, int64_t H,
+                              const void* residual, const void* post_weight, const void* gate,
+                              int64_t gate_rows, float alpha, const void* pre_weight, float eps,
+                              float weight_offset, void* h, void* y, void* y_codes,
+                              void* y_scales_f32, void* stream) {
+  if (!x || T <= 0 || H <= 0 || H % 8 || !(eps >= 0.0f)) return APEX_ERR_INVALID_ARG;
+  if (!h && !y && !y_codes) return APEX_ERR_INVALID_ARG;
+  if ((y || y_codes) && !pre_weight) return APEX_ERR_INVALID_ARG;
+  if (y_codes && (!y_scales_f32 || H % 16)) return APEX_ERR_INVALID_ARG;
+  if (gate && (gate_rows <= 0 || T % gate_rows)) return APEX_ERR_INVALID_ARG;
+  if (!is_16bit(dtype) || H > 32768 || T >= (1ll << 31)) return APEX_ERR_UNSUPPORTED;
+  for (const void* p : {x, residual, post_weight, gate, pre_weight, (const void*)h,
+                        (const void*)y, (const void*)y_codes})
+    if (!aligned(p, 16)) return APEX_ERR_ALIGNMENT;
+  if (!aligned(y_scales_f32, 4)) return APEX_ERR_ALIGNMENT;
+  apex::NormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.post = post_weight;
+  a.gate = gate;
+  a.pre = (y || y_codes) ? pre_weight : nullptr;
+  a.T = (int)T;
+  a.H = (int)H;
+  a.G = (int)ceil_div(H, 128);
+  a.rows_per_gate = gate ? (int)(T / gate_rows) : 1;
+  a.alpha = alpha;
+  a.eps = eps;
+  a.off = weight_offset;
+  a.h = h;
+  a.y = y;
+  a.codes = static_cast<uint8_t*>(y_codes);
+  a.scales = static_cast<float*>(y_scales_f32);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto kern, int nc) {
+    const unsigned threads = (unsigned)(ceil_div(ceil_div(H, 8 * nc), 32) * 32);
+    return launched(launch_pdl(kern, (unsigned)T, threads, 0, s, a));
+  };
+  auto by_width = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (H <= 8192) return run(apex::block_norm_kernel<DT, 1>, 1);
+    if (H <= 16384) return run(apex::block_norm_kernel<DT, 2>, 2);
+    return run(apex::block_norm_kernel<DT, 4>, 4);
+  };
+  return dtype == APEX_DTYPE_F16 ? by_width(std::integral_constant<int, apex::DT_F16>{})
+                                 : by_width(std::integral_constant<int, apex::DT_BF16>{});
+}
+
+}  // extern "C"

@@ -1,0 +1,347 @@
+"""Block-scaled FP8, expert and block-norm entry points of the C ABI (include/apex_w4a4.h).
+
+As in the package itself, every ``apex_*`` function has the name and arguments of the C entry
+point with torch CUDA tensors for device pointers, and the functions without the prefix
+allocate their outputs and workspaces (from torch's caching allocator, on the call's stream).
+Tensors are contiguous and on one device, which the call makes current while it launches;
+``stream`` defaults to that device's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+APEX_DTYPE_F16 = 0
+APEX_DTYPE_BF16 = 1
+APEX_DTYPE_F32 = 2
+APEX_SCORE_SOFTMAX = 0
+APEX_SCORE_SIGMOID = 1
+APEX_MAX_EXPERTS = 512
+APEX_MAX_TOP_K = 32
+
+ENTRY_POINTS = [
+    "apex_quantize_act_fp8_block", "apex_pack_weights_fp8_block", "apex_gemm_fp8_block",
+    "apex_linear_fp8_block", "apex_linear_fp8_block_workspace_size", "apex_route_experts",
+    "apex_plan_experts", "apex_moe_mlp_fp8_block", "apex_moe_mlp_fp8_block_workspace_size",
+    "apex_block_norm",
+]
+CONVENIENCES = [
+    "quantize_act_fp8_block", "pack_weights_fp8_block", "gemm_fp8_block", "linear_fp8_block",
+    "route_experts", "plan_experts", "moe_mlp_fp8_block", "block_norm",
+]
+__all__ = ENTRY_POINTS + CONVENIENCES
+
+_DTYPES = {torch.float16: APEX_DTYPE_F16, torch.bfloat16: APEX_DTYPE_BF16,
+           torch.float32: APEX_DTYPE_F32}
+_SCORES = {"softmax": APEX_SCORE_SOFTMAX, "sigmoid": APEX_SCORE_SIGMOID}
+
+
+def declare(lib):
+    """ctypes signatures (called once by load_library)."""
+    P, I32, I64, SZ, F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
+                          ctypes.c_float)
+    for name, args in {
+        "apex_quantize_act_fp8_block": [P, I32, I64, I64, P, P, P],
+        "apex_pack_weights_fp8_block": [P, I32, I64, I64, I64, P, P, P],
+        "apex_gemm_fp8_block": [I64, I64, I64, P, P, P, P, I32, P, P],
+        "apex_linear_fp8_block": [I64, I64, I64, P, I32, P, P, P, P, SZ, P],
+        "apex_route_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P],
+        "apex_plan_experts": [P, I64, I32, I32, P, P, P],
+        "apex_moe_mlp_fp8_block": [I64, I32, I32, I64, I64, P, I32, P, P, P, P, P, P, P, P, P, P,
+                                   SZ, P],
+        "apex_block_norm": [P, I32, I64, I64, P, P, P, I64, F, P, F, F, P, P, P, P, P],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
+    lib.apex_linear_fp8_block_workspace_size.argtypes = [I64, I64, I64]
+    lib.apex_linear_fp8_block_workspace_size.restype = SZ
+    lib.apex_moe_mlp_fp8_block_workspace_size.argtypes = [I64, I32, I32, I64, I64]
+    lib.apex_moe_mlp_fp8_block_workspace_size.restype = SZ
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _call(name, tensors, args, stream):
+    """Launch entry point `name`: `tensors` are the tensor arguments (None where absent), all on
+    one device; `args(p)` lists the C arguments but the stream, p the device pointers."""
+    from . import ApexError
+    device = None
+    pointers = []
+    for t in tensors:
+        if t is None:
+            pointers.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor (device memory)")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        index = t.get_device()
+        if device is None:
+            device = index
+        elif device != index:
+            raise ValueError("expected tensors on one device")
+        pointers.append(t.data_ptr())
+    fn = getattr(_lib(), name)
+    if stream is not None and stream.device_index != device:
+        raise ValueError("expected a stream of the tensors' device")
+    if device == torch.cuda.current_device():
+        s = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+        code = fn(*args(pointers), s)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+            code = fn(*args(pointers), s)
+    if code != 0:
+        raise ApexError(code, name)
+
+
+def _dtype(t):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected fp16, bf16 or fp32, got {t.dtype}") from None
+
+
+def _expect(t, name, dtype, shape):
+    """Shape and type of a tensor argument of a convenience function."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _scratch(nbytes, like, stream):
+    """Workspace bytes from the caching allocator; when the work runs on another stream than the
+    allocator's current one, the block is kept until that stream has passed."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _empty(shape, dtype, like, stream):
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+# ------------------------------------------------------------------ the C entry points
+
+def apex_quantize_act_fp8_block(x, M, K, codes, scales_f32, stream=None):
+    _call("apex_quantize_act_fp8_block", (x, codes, scales_f32),
+          lambda p: (p[0], _dtype(x), M, K, p[1], p[2]), stream)
+
+
+def apex_pack_weights_fp8_block(w, E, N, K, codes, scales_f32, stream=None):
+    _call("apex_pack_weights_fp8_block", (w, codes, scales_f32),
+          lambda p: (p[0], _dtype(w), E, N, K, p[1], p[2]), stream)
+
+
+def apex_gemm_fp8_block(M, N, K, a_codes, a_scales, w_codes, w_scales, y, stream=None):
+    _call("apex_gemm_fp8_block", (a_codes, a_scales, w_codes, w_scales, y),
+          lambda p: (M, N, K, p[0], p[1], p[2], p[3], _dtype(y), p[4]), stream)
+
+
+def apex_linear_fp8_block_workspace_size(M, N, K) -> int:
+    return int(_lib().apex_linear_fp8_block_workspace_size(M, N, K))
+
+
+def apex_linear_fp8_block(M, N, K, x, w_codes, w_scales, y, workspace, workspace_bytes=None,
+                          stream=None):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _call("apex_linear_fp8_block", (x, w_codes, w_scales, y, workspace),
+          lambda p: (M, N, K, p[0], _dtype(x), p[1], p[2], p[3], p[4], workspace_bytes), stream)
+
+
+def apex_route_experts(logits, T, E, k, score, bias_f32, groups, topk_groups, renormalize, scale,
+                       mask_u8, weights_f32, ids_i32, stream=None):
+    _call("apex_route_experts", (logits, bias_f32, mask_u8, weights_f32, ids_i32),
+          lambda p: (p[0], _dtype(logits), T, E, k, score, p[1], groups, topk_groups,
+                     1 if renormalize else 0, scale, p[2], p[3], p[4]), stream)
+
+
+def apex_plan_experts(ids_i32, T, k, E, offsets_i32, order_i32, stream=None):
+    _call("apex_plan_experts", (ids_i32, offsets_i32, order_i32),
+          lambda p: (p[0], T, k, E, p[1], p[2]), stream)
+
+
+def apex_moe_mlp_fp8_block_workspace_size(T, E, k, H, I) -> int:
+    return int(_lib().apex_moe_mlp_fp8_block_workspace_size(T, E, k, H, I))
+
+
+def apex_moe_mlp_fp8_block(T, E, k, H, I, x, weights_f32, ids_i32, offsets_i32, order_i32,
+                           w13_codes, w13_scales, w2_codes, w2_scales, y, workspace,
+                           workspace_bytes=None, stream=None):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _call("apex_moe_mlp_fp8_block",
+          (x, weights_f32, ids_i32, offsets_i32, order_i32, w13_codes, w13_scales, w2_codes,
+           w2_scales, y, workspace),
+          lambda p: (T, E, k, H, I, p[0], _dtype(x), *p[1:], workspace_bytes), stream)
+
+
+def apex_block_norm(x, T, H, residual, post_weight, gate, gate_rows, alpha, pre_weight, eps,
+                    weight_offset, h, y, y_codes, y_scales_f32, stream=None):
+    _call("apex_block_norm",
+          (x, residual, post_weight, gate, pre_weight, h, y, y_codes, y_scales_f32),
+          lambda p: (p[0], _dtype(x), T, H, p[1], p[2], p[3], gate_rows, alpha, p[4], eps,
+                     weight_offset, p[5], p[6], p[7], p[8]), stream)
+
+
+# ------------------------------------------------------------------ tensor conveniences
+
+def quantize_act_fp8_block(x, stream=None):
+    """fp16 / bf16 [M, K] -> (E4M3 codes uint8 [M, K], scales fp32 [M, ceil(K/128)])."""
+    M, K = x.shape
+    codes = _empty((M, K), torch.uint8, x, stream)
+    scales = _empty((M, -(-K // 128)), torch.float32, x, stream)
+    if M:
+        apex_quantize_act_fp8_block(x, M, K, codes, scales, stream)
+    return codes, scales
+
+
+def pack_weights_fp8_block(w, stream=None):
+    """fp16 / bf16 / fp32 [..., N, K] -> (E4M3 codes uint8 of w's shape, scales fp32
+    [..., ceil(N/128), ceil(K/128)])."""
+    N, K = w.shape[-2:]
+    codes = _empty(w.shape, torch.uint8, w, stream)
+    scales = _empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), torch.float32, w, stream)
+    if w.numel():
+        apex_pack_weights_fp8_block(w, w.numel() // (N * K), N, K, codes, scales, stream)
+    return codes, scales
+
+
+def gemm_fp8_block(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None,
+                   stream=None):
+    """Y = block-scaled FP8 GEMM of quantized operands -> [M, N] of `dtype`."""
+    M, K = a_codes.shape
+    N = w_codes.shape[0]
+    G = -(-K // 128)
+    _expect(a_codes, "a_codes", torch.uint8, (M, K))
+    _expect(a_scales, "a_scales", torch.float32, (M, G))
+    _expect(w_codes, "w_codes", torch.uint8, (N, K))
+    _expect(w_scales, "w_scales", torch.float32, (-(-N // 128), G))
+    if out is None:
+        out = _empty((M, N), dtype, a_codes, stream)
+    else:
+        _expect(out, "out", out.dtype, (M, N))
+    if M:
+        apex_gemm_fp8_block(M, N, K, a_codes, a_scales, w_codes, w_scales, out, stream)
+    return out
+
+
+def linear_fp8_block(x, w_codes, w_scales, out=None, stream=None):
+    """y = x . W^T for x fp16 / bf16 [M, K], W from pack_weights_fp8_block -> [M, N] like x."""
+    M, K = x.shape
+    N = w_codes.shape[0]
+    _expect(w_codes, "w_codes", torch.uint8, (N, K))
+    _expect(w_scales, "w_scales", torch.float32, (-(-N // 128), -(-K // 128)))
+    if out is None:
+        out = _empty((M, N), x.dtype, x, stream)
+    else:
+        _expect(out, "out", x.dtype, (M, N))
+    if M:
+        nbytes = apex_linear_fp8_block_workspace_size(M, N, K)
+        apex_linear_fp8_block(M, N, K, x, w_codes, w_scales, out,
+                              _scratch(max(nbytes, 16), x, stream), nbytes, stream)
+    return out
+
+
+def route_experts(logits, k, bias=None, score="softmax", groups=1, topk_groups=1,
+                  renormalize=True, scale=1.0, mask=None, plan=False, stream=None):
+    """logits [T, E] -> (weights fp32 [T, k], ids int32 [T, k]); with plan also (offsets, order)
+    of plan_experts.  bias fp32 [E]; mask bool [T] (False: the token takes no part)."""
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, (E,))
+    if mask is not None:
+        _expect(mask, "mask", torch.bool, (T,))
+    weights = _empty((T, k), torch.float32, logits, stream)
+    ids = _empty((T, k), torch.int32, logits, stream)
+    if T:
+        apex_route_experts(logits, T, E, k, _SCORES[score], bias, groups, topk_groups,
+                           renormalize, scale, mask, weights, ids, stream)
+    return (weights, ids, *plan_experts(ids, E, stream)) if plan else (weights, ids)
+
+
+def plan_experts(ids, experts, stream=None):
+    """ids int32 [T, k] -> (offsets int32 [experts + 1], order int32 [T * k])."""
+    T, k = ids.shape
+    _expect(ids, "ids", torch.int32, (T, k))
+    offsets = _empty((experts + 1,), torch.int32, ids, stream)
+    order = _empty((T * k,), torch.int32, ids, stream)
+    if T:
+        apex_plan_experts(ids, T, k, experts, offsets, order, stream)
+    else:
+        with torch.cuda.stream(stream):   # None: the current one
+            offsets.zero_()
+    return offsets, order
+
+
+def moe_mlp_fp8_block(x, weights, ids, offsets, order, w13_codes, w13_scales, w2_codes,
+                      w2_scales, out=None, stream=None):
+    """The experts' gated MLP of x fp16 / bf16 [T, H] -> [T, H] like x.  weights, ids, offsets,
+    order from route_experts(..., plan=True); w13 [E, 2, I, H] (gate, up) and w2 [E, H, I] from
+    pack_weights_fp8_block."""
+    T, H = x.shape
+    k = ids.shape[1]
+    E, I = w13_codes.shape[0], w13_codes.shape[2]
+    GH, GI = -(-H // 128), -(-I // 128)
+    _expect(weights, "weights", torch.float32, (T, k))
+    _expect(ids, "ids", torch.int32, (T, k))
+    _expect(offsets, "offsets", torch.int32, (E + 1,))
+    _expect(order, "order", torch.int32, (T * k,))
+    _expect(w13_codes, "w13_codes", torch.uint8, (E, 2, I, H))
+    _expect(w13_scales, "w13_scales", torch.float32, (E, 2, GI, GH))
+    _expect(w2_codes, "w2_codes", torch.uint8, (E, H, I))
+    _expect(w2_scales, "w2_scales", torch.float32, (E, GH, GI))
+    if out is None:
+        out = _empty((T, H), x.dtype, x, stream)
+    else:
+        _expect(out, "out", x.dtype, (T, H))
+    if T:
+        nbytes = apex_moe_mlp_fp8_block_workspace_size(T, E, k, H, I)
+        apex_moe_mlp_fp8_block(T, E, k, H, I, x, weights, ids, offsets, order, w13_codes,
+                               w13_scales, w2_codes, w2_scales, out,
+                               _scratch(max(nbytes, 16), x, stream), nbytes, stream)
+    return out
+
+
+def block_norm(x, pre_weight=None, residual=None, post_weight=None, gate=None, alpha=1.0,
+               eps=1e-6, weight_offset=0.0, out="codes", stream=None):
+    """x [T, H] -> (h, y, codes, scales): the norm behind a block, gate, scaled residual and the
+    norm before the next one.  out: "codes" (y None), "values" (codes and scales None), "both", or
+    "residual" (h alone, without the second norm).  gate [rows, H], rows dividing T."""
+    T, H = x.shape
+    if out not in ("codes", "values", "both", "residual"):
+        raise ValueError(f"out: expected codes, values, both or residual, got {out!r}")
+    if out != "residual" and pre_weight is None:
+        raise ValueError(f"out={out!r} needs pre_weight")
+    if residual is not None:
+        _expect(residual, "residual", x.dtype, (T, H))
+    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
+        if w is not None:
+            _expect(w, name, x.dtype, (H,))
+    rows = 0
+    if gate is not None:
+        rows = gate.shape[0]
+        _expect(gate, "gate", x.dtype, (rows, H))
+    h = _empty((T, H), x.dtype, x, stream)
+    y = _empty((T, H), x.dtype, x, stream) if out in ("values", "both") else None
+    codes = scales = None
+    if out in ("codes", "both"):
+        codes = _empty((T, H), torch.uint8, x, stream)
+        scales = _empty((T, -(-H // 128)), torch.float32, x, stream)
+    if T:
+        apex_block_norm(x, T, H, residual, post_weight, gate, rows, alpha, pre_weight, eps,
+                        weight_offset, h, y, codes, scales, stream)
+    return h, y, codes, scales

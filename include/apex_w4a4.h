@@ -408,6 +408,120 @@ apex_status_t apex_w4a4_gemm_fp8_dual(int64_t M, int64_t N, int64_t K, int32_t g
                                       const void *w_out_f16, int32_t Cp, void *y_f16,
                                       void *stream);
 
+/*
+ * ---- Block-scaled FP8 (E4M3): activations quantized online in groups of 1 x 128, weights
+ * offline in blocks of 128 x 128, one fp32 scale each.  For a group or block with largest
+ * magnitude a:
+ *   s = fp32_rne(a / 448),  q = E4M3(x / s): the exact quotient rounded once, half to even,
+ *   saturating at 448; q = 0 when s == 0.
+ * A NaN makes its group's scale and codes NaN; an infinity makes the scale infinite and the
+ * group's products NaN.
+ * 16-bit tensors are fp16 or bf16 (APEX_DTYPE_*).  The inner size K is a multiple of 16 (the
+ * last group may be ragged), every other size is free.  K, N <= 2^20.  Codes and 16-bit
+ * tensors are 16-byte aligned unless stated, fp32 and int32 ones 4-byte.
+ */
+#define APEX_DTYPE_F16 0
+#define APEX_DTYPE_BF16 1
+#define APEX_DTYPE_F32 2
+
+/* x [M][K] (fp16 / bf16) -> codes [M][K] bytes, scales fp32 [M][ceil(K/128)]. */
+apex_status_t apex_quantize_act_fp8_block(const void *x, int32_t dtype, int64_t M, int64_t K,
+                                          void *codes, void *scales_f32, void *stream);
+
+/* w [E][N][K] (fp16 / bf16 / fp32; E = 1 for one matrix) -> codes [E][N][K], scales fp32
+ * [E][ceil(N/128)][ceil(K/128)]. */
+apex_status_t apex_pack_weights_fp8_block(const void *w, int32_t dtype, int64_t E, int64_t N,
+                                          int64_t K, void *codes, void *scales_f32, void *stream);
+
+/*
+ * y [M][N] (fp16 / bf16, 2-byte aligned) = sum_g P_g[m,n] * a_scales[m,g] * w_scales[n/128,g],
+ * P_g the product over the 128-wide K-group g, everything accumulated in fp32 and rounded once.
+ * Any finite, infinite or NaN codes and scales are multiplied as they are.
+ */
+apex_status_t apex_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void *a_codes,
+                                  const void *a_scales, const void *w_codes,
+                                  const void *w_scales, int32_t dtype, void *y, void *stream);
+
+/* Quantizer and GEMM in one call: y [M][N] of x's type.  workspace: 256-byte aligned device
+ * memory of apex_linear_fp8_block_workspace_size bytes, need not be cleared; calls that share
+ * one must not run concurrently. */
+size_t apex_linear_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K);
+apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void *x, int32_t dtype,
+                                    const void *w_codes, const void *w_scales, void *y,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- Experts.  Routing: for every token t with logits z[E] (fp16 / bf16 / fp32),
+ *   p = softmax(z) or 1 / (1 + exp(-z));  v = p + bias (bias may be NULL)
+ *   groups > 1: of the groups of E/groups neighbouring experts, the topk_groups with the
+ *     largest sum of their two largest v (one, where a group has one) stay in the choice
+ *   ids [T][k] = the k largest v in descending order, ties to the lowest index
+ *   weights [T][k] = scale * p[ids] (divided by their sum first with renormalize)
+ * The choice is that of the exact scores: values are compared in 64 bits (the logits themselves
+ * where there is neither a bias nor groups).  mask [T] bytes (NULL: all ones): a token with 0
+ * gets ids -1 and weights 0.  NaN logits are chosen last and make weights NaN; a softmax row of
+ * -inf alone has scores 0, and weights that sum to 0 stay 0.
+ * E % groups == 0, k <= topk_groups * E / groups, E <= APEX_MAX_EXPERTS, k <= APEX_MAX_TOP_K,
+ * groups <= 32.
+ */
+#define APEX_MAX_EXPERTS 512
+#define APEX_MAX_TOP_K 32
+#define APEX_SCORE_SOFTMAX 0
+#define APEX_SCORE_SIGMOID 1
+apex_status_t apex_route_experts(const void *logits, int32_t dtype, int64_t T, int32_t E,
+                                 int32_t k, int32_t score, const void *bias_f32, int32_t groups,
+                                 int32_t topk_groups, int32_t renormalize, float scale,
+                                 const void *mask_u8, void *weights_f32, void *ids_i32,
+                                 void *stream);
+
+/*
+ * Groups the choices by expert: order [T*k] lists the flat indices t*k + j with ids[t][j] == 0
+ * in ascending order, then those of expert 1, ...; expert e's are order[offsets[e] ..
+ * offsets[e+1]-1] (offsets [E+1]).  Ids outside [0, E) belong to no expert; the entries of
+ * order behind offsets[E] are -1.
+ */
+apex_status_t apex_plan_experts(const void *ids_i32, int64_t T, int32_t k, int32_t E,
+                                void *offsets_i32, void *order_i32, void *stream);
+
+/*
+ * The experts' products: x [T][H] (fp16 / bf16) is quantized (1 x 128 groups), and
+ *   h = silu(x . Wg[e]^T) * (x . Wu[e]^T), quantized in groups of 128 from its fp32 values,
+ *   y[t] = sum_j weights[t][j] * (h . W2[e]^T), e = ids[t][j], over the ids in [0, E),
+ * with each product rounded to x's type before the fp32 sum over j.  A token without experts
+ * gets zeros.
+ *   w13 codes [E][2][I][H] (gate, up), scales [E][2][ceil(I/128)][ceil(H/128)];
+ *   w2 codes [E][H][I], scales [E][ceil(H/128)][ceil(I/128)]  (apex_pack_weights_fp8_block)
+ *   weights, ids: as from apex_route_experts; offsets, order: apex_plan_experts of these ids.
+ * H % 16 == 0, I % 16 == 0.  y [T][H] 16-byte aligned.  workspace: as for
+ * apex_linear_fp8_block.
+ */
+size_t apex_moe_mlp_fp8_block_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H,
+                                             int64_t I);
+apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                                     const void *x, int32_t dtype, const void *weights_f32,
+                                     const void *ids_i32, const void *offsets_i32,
+                                     const void *order_i32, const void *w13_codes,
+                                     const void *w13_scales, const void *w2_codes,
+                                     const void *w2_scales, void *y, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * What stands between two blocks, in one pass over x [T][H] (fp16 / bf16, the block's output):
+ *   z = x;  with post_weight [H]: z = z * rsqrt(mean(z^2) + eps) * (weight_offset + post_weight)
+ *   with gate [gate_rows][H]: z = z * gate[t / (T / gate_rows)]  (T % gate_rows == 0)
+ *   h = residual + alpha * z  (residual [T][H] may be NULL: h = alpha * z)
+ *   y = h * rsqrt(mean(h^2) + eps) * (weight_offset + pre_weight)
+ * in fp32; h [T][H] and y [T][H] rounded to x's type, y_codes [T][H] and y_scales
+ * [T][ceil(H/128)] as apex_quantize_act_fp8_block would make them from the unrounded y.
+ * Outputs may be NULL (not all; y and y_codes need pre_weight).  h may be the residual's own
+ * memory.  H % 8 == 0 (16 with y_codes), H <= 32768.  All but the scales 16-byte aligned.
+ */
+apex_status_t apex_block_norm(const void *x, int32_t dtype, int64_t T, int64_t H,
+                              const void *residual, const void *post_weight, const void *gate,
+                              int64_t gate_rows, float alpha, const void *pre_weight, float eps,
+                              float weight_offset, void *h, void *y, void *y_codes,
+                              void *y_scales_f32, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
