@@ -35,8 +35,8 @@ __all__ = [
     "pack_weights", "quantize_act", "gemm", "workspace",
     "apex_quantize_act_fp8_block", "apex_pack_weights_fp8_block", "apex_gemm_fp8_block",
     "apex_linear_fp8_block", "apex_linear_fp8_block_workspace_size", "apex_route_experts",
-    "apex_plan_experts", "apex_moe_mlp_fp8_block", "apex_moe_mlp_fp8_block_workspace_size",
-    "apex_block_norm", "quantize_act_fp8_block", "pack_weights_fp8_block", "gemm_fp8_block",
+    "apex_plan_experts", "apex_route_plan_experts", "apex_moe_mlp_fp8_block",
+    "apex_moe_mlp_fp8_block_workspace_size", "apex_block_norm", "quantize_act_fp8_block", "pack_weights_fp8_block", "gemm_fp8_block",
     "linear_fp8_block", "route_experts", "plan_experts", "moe_mlp_fp8_block", "block_norm",
 ]
 

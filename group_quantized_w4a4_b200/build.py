@@ -1,4 +1,5 @@
-"""Build the CUDA library (sm_100a) in-tree: group_quantized_w4a4_b200/_lib/libapex_w4a4.so.
+"""Build the CUDA library (sm_100a) in-tree: group_quantized_w4a4_b200/_lib/libapex_w4a4.so,
+and the torch side of its newer calls, _lib/apex_torch.so (plain C++ against torch's headers).
 
     python -m group_quantized_w4a4_b200.build [--force]
 
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libapex_w4a4.so")
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "apex_torch.so")
+TORCH_SRC = os.path.join(CSRC, "torch_binding.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -58,5 +61,36 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def torch_is_stale() -> bool:
+    if not os.path.exists(TORCH_LIB_PATH):
+        return True
+    t = os.path.getmtime(TORCH_LIB_PATH)
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    return any(os.path.getmtime(s) > t for s in [TORCH_SRC, *headers])
+
+
+def build_torch(force: bool = False) -> str:
+    """Compile the torch binding if it is older than its sources (or `force`); return its path."""
+    if not force and not torch_is_stale():
+        return TORCH_LIB_PATH
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
+    include = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cxx = shutil.which("g++") or "g++"
+    subprocess.run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    *(f for i in include for f in ("-isystem", i)), TORCH_SRC, "-o", tmp,
+                    f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                    "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, TORCH_LIB_PATH)
+    return TORCH_LIB_PATH
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_torch(force="--force" in sys.argv))

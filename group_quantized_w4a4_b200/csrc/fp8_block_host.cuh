@@ -150,6 +150,105 @@ apex_status_t check_moe(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
   return APEX_OK;
 }
 
+// ------------------------------------------------------------------ routing
+
+// Up to this many tokens one CTA of 16 warps routes and groups them (one launch instead of two;
+// four tokens a warp at most).
+constexpr int64_t kRoutePlanTokens = 64;
+constexpr int kRoutePlanWarps = 16;
+// From this many choices on a cluster of 8 CTAs groups them.
+constexpr int64_t kPlanClusterChoices = 4096;
+
+apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, int64_t T,
+                         int32_t E, int32_t k, int32_t score, const void* bias_f32,
+                         int32_t groups, int32_t topk_groups, int32_t renormalize, float scale,
+                         const void* mask_u8, void* weights_f32, void* ids_i32) {
+  if (!logits || !weights_f32 || !ids_i32 || T <= 0 || E <= 0 || k <= 0 || groups <= 0 ||
+      topk_groups <= 0 || topk_groups > groups || E % groups)
+    return APEX_ERR_INVALID_ARG;
+  if (score != APEX_SCORE_SOFTMAX && score != APEX_SCORE_SIGMOID) return APEX_ERR_INVALID_ARG;
+  if (k > topk_groups * (E / groups)) return APEX_ERR_INVALID_ARG;
+  if (!is_float(dtype) || E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || groups > 32 ||
+      T >= kMaxSlots || T * (int64_t)k >= kMaxSlots)
+    return APEX_ERR_UNSUPPORTED;
+  if (!aligned(logits, dtype == APEX_DTYPE_F32 ? 4 : 2) || !aligned(bias_f32, 4) ||
+      !aligned(weights_f32, 4) || !aligned(ids_i32, 4))
+    return APEX_ERR_ALIGNMENT;
+  a->logits = logits;
+  a->bias = static_cast<const float*>(bias_f32);
+  a->mask = static_cast<const uint8_t*>(mask_u8);
+  a->T = (int)T;
+  a->E = E;
+  a->k = k;
+  a->G = groups;
+  a->TG = topk_groups;
+  a->sigmoid = score == APEX_SCORE_SIGMOID;
+  a->renorm = renormalize != 0;
+  a->scale = scale;
+  a->ids = static_cast<int32_t*>(ids_i32);
+  a->weights = static_cast<float*>(weights_f32);
+  return APEX_OK;
+}
+
+template <int DT, int EPL>
+apex_status_t route_launch_t(const apex::RouteArgs& a, int32_t* offsets, int32_t* order,
+                             cudaStream_t s) {
+  if (offsets) {
+    auto kern = apex::route_plan_kernel<DT, EPL>;
+    const int warps = kRoutePlanWarps;
+    const int route = a.G > 1 ? warps * a.E * 8 : 0, plan = apex::plan_smem(a.E, warps);
+    constexpr int most = kRoutePlanWarps * APEX_MAX_EXPERTS * 8;
+    static thread_local int attr_dev = -1;
+    if (set_smem(kern, most, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
+    return launched(launch_pdl(kern, 1u, 32u * warps, (size_t)(route > plan ? route : plan), s, a,
+                               offsets, order));
+  }
+  int64_t blocks = ceil_div(a.T, apex::kRouteWarps);
+  const int64_t cap = (int64_t)dev_info().sms * 16;
+  if (blocks > cap) blocks = cap;
+  return launched(launch_pdl(apex::route_kernel<DT, EPL>, (unsigned)blocks,
+                             32 * apex::kRouteWarps,
+                             a.G > 1 ? (size_t)apex::kRouteWarps * a.E * 8 : 0, s, a));
+}
+
+template <int DT>
+apex_status_t route_launch_e(const apex::RouteArgs& a, int32_t* offsets, int32_t* order,
+                             cudaStream_t s) {
+  if (a.E <= 64) return route_launch_t<DT, 2>(a, offsets, order, s);
+  if (a.E <= 128) return route_launch_t<DT, 4>(a, offsets, order, s);
+  if (a.E <= 256) return route_launch_t<DT, 8>(a, offsets, order, s);
+  return route_launch_t<DT, 16>(a, offsets, order, s);
+}
+
+apex_status_t route_launch(const apex::RouteArgs& a, int32_t dtype, int32_t* offsets,
+                           int32_t* order, cudaStream_t s) {
+  if (dtype == APEX_DTYPE_F16) return route_launch_e<apex::DT_F16>(a, offsets, order, s);
+  if (dtype == APEX_DTYPE_BF16) return route_launch_e<apex::DT_BF16>(a, offsets, order, s);
+  return route_launch_e<apex::DT_F32>(a, offsets, order, s);
+}
+
+apex_status_t check_plan(const void* ids, int64_t T, int32_t k, int32_t E, const void* offsets,
+                         const void* order) {
+  if (!ids || !offsets || !order || T <= 0 || k <= 0 || E <= 0) return APEX_ERR_INVALID_ARG;
+  if (E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || T >= kMaxSlots || T * (int64_t)k >= kMaxSlots)
+    return APEX_ERR_UNSUPPORTED;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4)) return APEX_ERR_ALIGNMENT;
+  return APEX_OK;
+}
+
+apex_status_t plan_launch(const int32_t* ids, int64_t S, int32_t E, int32_t* offsets,
+                          int32_t* order, cudaStream_t s) {
+  const unsigned ctas = S >= kPlanClusterChoices ? 8u : 1u;
+  const int warps = 32;
+  static thread_local int attr_dev = -1;
+  if (set_smem(apex::plan_kernel, apex::plan_smem(APEX_MAX_EXPERTS, warps), &attr_dev) !=
+      cudaSuccess)
+    return launched(cudaErrorUnknown);
+  return launched(launch_pdl_cl(apex::plan_kernel, ctas, 32u * warps,
+                                (size_t)apex::plan_smem(E, warps), s, ctas, ids, (int)S, (int)E,
+                                offsets, order));
+}
+
 }  // namespace
 
 extern "C" {
@@ -229,64 +328,40 @@ apex_status_t apex_route_experts(const void* logits, int32_t dtype, int64_t T, i
                                  int32_t topk_groups, int32_t renormalize, float scale,
                                  const void* mask_u8, void* weights_f32, void* ids_i32,
                                  void* stream) {
-  if (!logits || !weights_f32 || !ids_i32 || T <= 0 || E <= 0 || k <= 0 || groups <= 0 ||
-      topk_groups <= 0 || topk_groups > groups || E % groups)
-    return APEX_ERR_INVALID_ARG;
-  if (score != APEX_SCORE_SOFTMAX && score != APEX_SCORE_SIGMOID) return APEX_ERR_INVALID_ARG;
-  if (k > topk_groups * (E / groups)) return APEX_ERR_INVALID_ARG;
-  if (!is_float(dtype) || E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || groups > 32 ||
-      T * (int64_t)k >= kMaxSlots)
-    return APEX_ERR_UNSUPPORTED;
-  if (!aligned(logits, dtype == APEX_DTYPE_F32 ? 4 : 2) || !aligned(bias_f32, 4) ||
-      !aligned(weights_f32, 4) || !aligned(ids_i32, 4))
-    return APEX_ERR_ALIGNMENT;
   apex::RouteArgs a;
-  a.logits = logits;
-  a.bias = static_cast<const float*>(bias_f32);
-  a.mask = static_cast<const uint8_t*>(mask_u8);
-  a.T = (int)T;
-  a.E = E;
-  a.k = k;
-  a.G = groups;
-  a.TG = topk_groups;
-  a.sigmoid = score == APEX_SCORE_SIGMOID;
-  a.renorm = renormalize != 0;
-  a.scale = scale;
-  a.ids = static_cast<int32_t*>(ids_i32);
-  a.weights = static_cast<float*>(weights_f32);
-  int64_t blocks = ceil_div(T, apex::kRouteWarps);
-  const int64_t cap = (int64_t)dev_info().sms * 16;
-  if (blocks > cap) blocks = cap;
-  const size_t smem = groups > 1 ? (size_t)apex::kRouteWarps * E * 8 : 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto run = [&](auto kern) {
-    return launched(launch_pdl(kern, (unsigned)blocks, 32 * apex::kRouteWarps, smem, s, a));
-  };
-  auto by_width = [&](auto dt) {
-    constexpr int DT = decltype(dt)::value;
-    if (E <= 64) return run(apex::route_kernel<DT, 2>);
-    if (E <= 128) return run(apex::route_kernel<DT, 4>);
-    if (E <= 256) return run(apex::route_kernel<DT, 8>);
-    return run(apex::route_kernel<DT, 16>);
-  };
-  if (dtype == APEX_DTYPE_F16) return by_width(std::integral_constant<int, apex::DT_F16>{});
-  if (dtype == APEX_DTYPE_BF16) return by_width(std::integral_constant<int, apex::DT_BF16>{});
-  return by_width(std::integral_constant<int, apex::DT_F32>{});
+  apex_status_t st = route_args(&a, logits, dtype, T, E, k, score, bias_f32, groups, topk_groups,
+                                renormalize, scale, mask_u8, weights_f32, ids_i32);
+  if (st != APEX_OK) return st;
+  return route_launch(a, dtype, nullptr, nullptr, static_cast<cudaStream_t>(stream));
 }
 
 apex_status_t apex_plan_experts(const void* ids_i32, int64_t T, int32_t k, int32_t E,
                                 void* offsets_i32, void* order_i32, void* stream) {
-  if (!ids_i32 || !offsets_i32 || !order_i32 || T <= 0 || k <= 0 || E <= 0)
-    return APEX_ERR_INVALID_ARG;
-  if (E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || T >= kMaxSlots || T * (int64_t)k >= kMaxSlots)
-    return APEX_ERR_UNSUPPORTED;
-  if (!aligned(ids_i32, 4) || !aligned(offsets_i32, 4) || !aligned(order_i32, 4))
-    return APEX_ERR_ALIGNMENT;
-  return launched(launch_pdl(apex::plan_kernel, (unsigned)(E + 1), 256, 0,
-                             static_cast<cudaStream_t>(stream),
-                             static_cast<const int32_t*>(ids_i32), (int)(T * k), (int)E,
-                             static_cast<int32_t*>(offsets_i32),
-                             static_cast<int32_t*>(order_i32)));
+  apex_status_t st = check_plan(ids_i32, T, k, E, offsets_i32, order_i32);
+  if (st != APEX_OK) return st;
+  return plan_launch(static_cast<const int32_t*>(ids_i32), T * k, E,
+                     static_cast<int32_t*>(offsets_i32), static_cast<int32_t*>(order_i32),
+                     static_cast<cudaStream_t>(stream));
+}
+
+apex_status_t apex_route_plan_experts(const void* logits, int32_t dtype, int64_t T, int32_t E,
+                                      int32_t k, int32_t score, const void* bias_f32,
+                                      int32_t groups, int32_t topk_groups, int32_t renormalize,
+                                      float scale, const void* mask_u8, void* weights_f32,
+                                      void* ids_i32, void* offsets_i32, void* order_i32,
+                                      void* stream) {
+  apex::RouteArgs a;
+  apex_status_t st = route_args(&a, logits, dtype, T, E, k, score, bias_f32, groups, topk_groups,
+                                renormalize, scale, mask_u8, weights_f32, ids_i32);
+  if (st == APEX_OK) st = check_plan(ids_i32, T, k, E, offsets_i32, order_i32);
+  if (st != APEX_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t* off = static_cast<int32_t*>(offsets_i32);
+  int32_t* order = static_cast<int32_t*>(order_i32);
+  if (T <= kRoutePlanTokens) return route_launch(a, dtype, off, order, s);
+  st = route_launch(a, dtype, nullptr, nullptr, s);
+  if (st != APEX_OK) return st;
+  return plan_launch(a.ids, T * k, E, off, order, s);
 }
 
 size_t apex_moe_mlp_fp8_block_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H,

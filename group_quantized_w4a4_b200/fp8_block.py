@@ -23,7 +23,7 @@ APEX_MAX_TOP_K = 32
 ENTRY_POINTS = [
     "apex_quantize_act_fp8_block", "apex_pack_weights_fp8_block", "apex_gemm_fp8_block",
     "apex_linear_fp8_block", "apex_linear_fp8_block_workspace_size", "apex_route_experts",
-    "apex_plan_experts", "apex_moe_mlp_fp8_block", "apex_moe_mlp_fp8_block_workspace_size",
+    "apex_plan_experts", "apex_route_plan_experts", "apex_moe_mlp_fp8_block", "apex_moe_mlp_fp8_block_workspace_size",
     "apex_block_norm",
 ]
 CONVENIENCES = [
@@ -47,6 +47,8 @@ def declare(lib):
         "apex_gemm_fp8_block": [I64, I64, I64, P, P, P, P, I32, P, P],
         "apex_linear_fp8_block": [I64, I64, I64, P, I32, P, P, P, P, SZ, P],
         "apex_route_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P],
+        "apex_route_plan_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P,
+                                    P, P],
         "apex_plan_experts": [P, I64, I32, I32, P, P, P],
         "apex_moe_mlp_fp8_block": [I64, I32, I32, I64, I64, P, I32, P, P, P, P, P, P, P, P, P, P,
                                    SZ, P],
@@ -107,28 +109,44 @@ def _dtype(t):
         raise ValueError(f"expected fp16, bf16 or fp32, got {t.dtype}") from None
 
 
-def _expect(t, name, dtype, shape):
-    """Shape and type of a tensor argument of a convenience function."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+# ------------------------------------------------------------------ the torch binding
+
+_native = None
+# the entry points that the binding calls, in the order of its table
+_BOUND = ["apex_quantize_act_fp8_block", "apex_gemm_fp8_block", "apex_linear_fp8_block",
+          "apex_linear_fp8_block_workspace_size", "apex_route_experts", "apex_plan_experts",
+          "apex_route_plan_experts", "apex_moe_mlp_fp8_block",
+          "apex_moe_mlp_fp8_block_workspace_size", "apex_block_norm"]
 
 
-def _scratch(nbytes, like, stream):
-    """Workspace bytes from the caching allocator; when the work runs on another stream than the
-    allocator's current one, the block is kept until that stream has passed."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+def _load():
+    """The compiled binding (csrc/torch_binding.cpp), built first if it is missing or stale."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
+
+        from . import ApexError, build
+        lib = _lib()
+        path = build.build_torch()
+        loader = importlib.machinery.ExtensionFileLoader("apex_torch", path)
+        spec = importlib.util.spec_from_loader("apex_torch", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND),
+                    ApexError)
+        _native = module
+    return _native
 
 
-def _empty(shape, dtype, like, stream):
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _run(name, stream, *args):
+    """Call `name` of the binding, on `stream` when one is given (its outputs and workspaces then
+    belong to that stream too)."""
+    fn = getattr(_native or _load(), name)
+    if stream is None:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 # ------------------------------------------------------------------ the C entry points
@@ -167,6 +185,15 @@ def apex_route_experts(logits, T, E, k, score, bias_f32, groups, topk_groups, re
                      1 if renormalize else 0, scale, p[2], p[3], p[4]), stream)
 
 
+def apex_route_plan_experts(logits, T, E, k, score, bias_f32, groups, topk_groups, renormalize,
+                            scale, mask_u8, weights_f32, ids_i32, offsets_i32, order_i32,
+                            stream=None):
+    _call("apex_route_plan_experts",
+          (logits, bias_f32, mask_u8, weights_f32, ids_i32, offsets_i32, order_i32),
+          lambda p: (p[0], _dtype(logits), T, E, k, score, p[1], groups, topk_groups,
+                     1 if renormalize else 0, scale, *p[2:]), stream)
+
+
 def apex_plan_experts(ids_i32, T, k, E, offsets_i32, order_i32, stream=None):
     _call("apex_plan_experts", (ids_i32, offsets_i32, order_i32),
           lambda p: (p[0], T, k, E, p[1], p[2]), stream)
@@ -199,92 +226,49 @@ def apex_block_norm(x, T, H, residual, post_weight, gate, gate_rows, alpha, pre_
 
 def quantize_act_fp8_block(x, stream=None):
     """fp16 / bf16 [M, K] -> (E4M3 codes uint8 [M, K], scales fp32 [M, ceil(K/128)])."""
-    M, K = x.shape
-    codes = _empty((M, K), torch.uint8, x, stream)
-    scales = _empty((M, -(-K // 128)), torch.float32, x, stream)
-    if M:
-        apex_quantize_act_fp8_block(x, M, K, codes, scales, stream)
-    return codes, scales
+    return _run("quantize_act", stream, x)
 
 
 def pack_weights_fp8_block(w, stream=None):
     """fp16 / bf16 / fp32 [..., N, K] -> (E4M3 codes uint8 of w's shape, scales fp32
     [..., ceil(N/128), ceil(K/128)])."""
     N, K = w.shape[-2:]
-    codes = _empty(w.shape, torch.uint8, w, stream)
-    scales = _empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), torch.float32, w, stream)
-    if w.numel():
-        apex_pack_weights_fp8_block(w, w.numel() // (N * K), N, K, codes, scales, stream)
+    with torch.cuda.stream(stream):   # None: the current one
+        codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        scales = torch.empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), dtype=torch.float32,
+                             device=w.device)
+        if w.numel():
+            apex_pack_weights_fp8_block(w, w.numel() // (N * K), N, K, codes, scales)
     return codes, scales
 
 
 def gemm_fp8_block(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None,
                    stream=None):
-    """Y = block-scaled FP8 GEMM of quantized operands -> [M, N] of `dtype`."""
-    M, K = a_codes.shape
-    N = w_codes.shape[0]
-    G = -(-K // 128)
-    _expect(a_codes, "a_codes", torch.uint8, (M, K))
-    _expect(a_scales, "a_scales", torch.float32, (M, G))
-    _expect(w_codes, "w_codes", torch.uint8, (N, K))
-    _expect(w_scales, "w_scales", torch.float32, (-(-N // 128), G))
-    if out is None:
-        out = _empty((M, N), dtype, a_codes, stream)
-    else:
-        _expect(out, "out", out.dtype, (M, N))
-    if M:
-        apex_gemm_fp8_block(M, N, K, a_codes, a_scales, w_codes, w_scales, out, stream)
-    return out
+    """Y = block-scaled FP8 GEMM of quantized operands -> [M, N] of `dtype` (fp16 or bf16)."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"dtype: expected fp16 or bf16, got {dtype}")
+    return _run("gemm", stream, a_codes, a_scales, w_codes, w_scales, dtype == torch.bfloat16,
+                out)
 
 
 def linear_fp8_block(x, w_codes, w_scales, out=None, stream=None):
     """y = x . W^T for x fp16 / bf16 [M, K], W from pack_weights_fp8_block -> [M, N] like x."""
-    M, K = x.shape
-    N = w_codes.shape[0]
-    _expect(w_codes, "w_codes", torch.uint8, (N, K))
-    _expect(w_scales, "w_scales", torch.float32, (-(-N // 128), -(-K // 128)))
-    if out is None:
-        out = _empty((M, N), x.dtype, x, stream)
-    else:
-        _expect(out, "out", x.dtype, (M, N))
-    if M:
-        nbytes = apex_linear_fp8_block_workspace_size(M, N, K)
-        apex_linear_fp8_block(M, N, K, x, w_codes, w_scales, out,
-                              _scratch(max(nbytes, 16), x, stream), nbytes, stream)
-    return out
+    return _run("linear", stream, x, w_codes, w_scales, out)
 
 
 def route_experts(logits, k, bias=None, score="softmax", groups=1, topk_groups=1,
                   renormalize=True, scale=1.0, mask=None, plan=False, stream=None):
     """logits [T, E] -> (weights fp32 [T, k], ids int32 [T, k]); with plan also (offsets, order)
     of plan_experts.  bias fp32 [E]; mask bool [T] (False: the token takes no part)."""
-    T, E = logits.shape
     if score not in _SCORES:
         raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
-    if bias is not None:
-        _expect(bias, "bias", torch.float32, (E,))
-    if mask is not None:
-        _expect(mask, "mask", torch.bool, (T,))
-    weights = _empty((T, k), torch.float32, logits, stream)
-    ids = _empty((T, k), torch.int32, logits, stream)
-    if T:
-        apex_route_experts(logits, T, E, k, _SCORES[score], bias, groups, topk_groups,
-                           renormalize, scale, mask, weights, ids, stream)
-    return (weights, ids, *plan_experts(ids, E, stream)) if plan else (weights, ids)
+    return _run("route", stream, logits, k, bias, _SCORES[score], groups, topk_groups,
+                renormalize, scale, mask, plan)
 
 
 def plan_experts(ids, experts, stream=None):
     """ids int32 [T, k] -> (offsets int32 [experts + 1], order int32 [T * k])."""
-    T, k = ids.shape
-    _expect(ids, "ids", torch.int32, (T, k))
-    offsets = _empty((experts + 1,), torch.int32, ids, stream)
-    order = _empty((T * k,), torch.int32, ids, stream)
-    if T:
-        apex_plan_experts(ids, T, k, experts, offsets, order, stream)
-    else:
-        with torch.cuda.stream(stream):   # None: the current one
-            offsets.zero_()
-    return offsets, order
+    return _run("plan", stream, ids, experts)
 
 
 def moe_mlp_fp8_block(x, weights, ids, offsets, order, w13_codes, w13_scales, w2_codes,
@@ -292,28 +276,12 @@ def moe_mlp_fp8_block(x, weights, ids, offsets, order, w13_codes, w13_scales, w2
     """The experts' gated MLP of x fp16 / bf16 [T, H] -> [T, H] like x.  weights, ids, offsets,
     order from route_experts(..., plan=True); w13 [E, 2, I, H] (gate, up) and w2 [E, H, I] from
     pack_weights_fp8_block."""
-    T, H = x.shape
-    k = ids.shape[1]
-    E, I = w13_codes.shape[0], w13_codes.shape[2]
-    GH, GI = -(-H // 128), -(-I // 128)
-    _expect(weights, "weights", torch.float32, (T, k))
-    _expect(ids, "ids", torch.int32, (T, k))
-    _expect(offsets, "offsets", torch.int32, (E + 1,))
-    _expect(order, "order", torch.int32, (T * k,))
-    _expect(w13_codes, "w13_codes", torch.uint8, (E, 2, I, H))
-    _expect(w13_scales, "w13_scales", torch.float32, (E, 2, GI, GH))
-    _expect(w2_codes, "w2_codes", torch.uint8, (E, H, I))
-    _expect(w2_scales, "w2_scales", torch.float32, (E, GH, GI))
-    if out is None:
-        out = _empty((T, H), x.dtype, x, stream)
-    else:
-        _expect(out, "out", x.dtype, (T, H))
-    if T:
-        nbytes = apex_moe_mlp_fp8_block_workspace_size(T, E, k, H, I)
-        apex_moe_mlp_fp8_block(T, E, k, H, I, x, weights, ids, offsets, order, w13_codes,
-                               w13_scales, w2_codes, w2_scales, out,
-                               _scratch(max(nbytes, 16), x, stream), nbytes, stream)
-    return out
+    return _run("moe", stream, x, weights, ids, offsets, order, w13_codes, w13_scales, w2_codes,
+                w2_scales, out)
+
+
+_NORM_OUT = {"codes": (False, True), "values": (True, False), "both": (True, True),
+             "residual": (False, False)}
 
 
 def block_norm(x, pre_weight=None, residual=None, post_weight=None, gate=None, alpha=1.0,
@@ -321,27 +289,9 @@ def block_norm(x, pre_weight=None, residual=None, post_weight=None, gate=None, a
     """x [T, H] -> (h, y, codes, scales): the norm behind a block, gate, scaled residual and the
     norm before the next one.  out: "codes" (y None), "values" (codes and scales None), "both", or
     "residual" (h alone, without the second norm).  gate [rows, H], rows dividing T."""
-    T, H = x.shape
-    if out not in ("codes", "values", "both", "residual"):
-        raise ValueError(f"out: expected codes, values, both or residual, got {out!r}")
+    if out not in _NORM_OUT:
+        raise ValueError(f"out: expected one of {sorted(_NORM_OUT)}, got {out!r}")
     if out != "residual" and pre_weight is None:
         raise ValueError(f"out={out!r} needs pre_weight")
-    if residual is not None:
-        _expect(residual, "residual", x.dtype, (T, H))
-    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-        if w is not None:
-            _expect(w, name, x.dtype, (H,))
-    rows = 0
-    if gate is not None:
-        rows = gate.shape[0]
-        _expect(gate, "gate", x.dtype, (rows, H))
-    h = _empty((T, H), x.dtype, x, stream)
-    y = _empty((T, H), x.dtype, x, stream) if out in ("values", "both") else None
-    codes = scales = None
-    if out in ("codes", "both"):
-        codes = _empty((T, H), torch.uint8, x, stream)
-        scales = _empty((T, -(-H // 128)), torch.float32, x, stream)
-    if T:
-        apex_block_norm(x, T, H, residual, post_weight, gate, rows, alpha, pre_weight, eps,
-                        weight_offset, h, y, codes, scales, stream)
-    return h, y, codes, scales
+    return _run("norm", stream, x, pre_weight, residual, post_weight, gate, alpha, eps,
+                weight_offset, *_NORM_OUT[out])

@@ -483,6 +483,14 @@ apex_status_t apex_route_experts(const void *logits, int32_t dtype, int64_t T, i
 apex_status_t apex_plan_experts(const void *ids_i32, int64_t T, int32_t k, int32_t E,
                                 void *offsets_i32, void *order_i32, void *stream);
 
+/* Both in one call, from the ids that it writes. */
+apex_status_t apex_route_plan_experts(const void *logits, int32_t dtype, int64_t T, int32_t E,
+                                      int32_t k, int32_t score, const void *bias_f32,
+                                      int32_t groups, int32_t topk_groups, int32_t renormalize,
+                                      float scale, const void *mask_u8, void *weights_f32,
+                                      void *ids_i32, void *offsets_i32, void *order_i32,
+                                      void *stream);
+
 /*
  * The experts' products: x [T][H] (fp16 / bf16) is quantized (1 x 128 groups), and
  *   h = silu(x . Wg[e]^T) * (x . Wu[e]^T), quantized in groups of 128 from its fp32 values,
