@@ -18,6 +18,7 @@
 #include "gemm.cuh"
 #include "gemm_f8.cuh"
 #include "gemm_f8_block.cuh"
+#include "gemm_f8_small.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
 #include "route.cuh"

@@ -101,27 +101,96 @@ FBArgs fb_args(int64_t M, int64_t N, int64_t K, const void* sa, const void* sw) 
   return a;
 }
 
-apex_status_t fb_dense(int64_t M, int64_t N, int64_t K, const void* a_codes, const void* a_scales,
-                       const void* w_codes, const void* w_scales, int32_t dtype, void* y,
-                       cudaStream_t s) {
-  FBArgs a = fb_args(M, N, K, a_scales, w_scales);
-  a.y = y;
-  a.y_vec = N % 8 == 0 && aligned(y, 16);
-  a.tiles_m = (int)ceil_div(M, 128);
+// ------------------------------------------------------------------ few tokens
+
+// Up to this many tokens (dense), or rows of an expert on average, the few-token kernel runs.
+constexpr int64_t kSmallTokens = 128;
+constexpr int64_t kSmallRows = 48;
+
+template <int BT, int KIND, int DT>
+apex_status_t launch_fs(const CUtensorMap& mw, const CUtensorMap& mx, const FBArgs& b,
+                        int64_t tiles, bool early, cudaStream_t s) {
+  using C = apex::FSCfg<BT, KIND>;
+  auto kern = apex::f8_small_gemm_kernel<BT, KIND, DT>;
+  static thread_local int attr_dev = -1;
+  if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
+  apex::FSArgs a;
+  a.b = b;
+  a.early = early ? 1 : 0;
+  // K split over a cluster while that leaves every CTA two groups and all CTAs resident
+  const int64_t room = (int64_t)dev_info().sms * C::CTAS_PER_SM;
+  a.S = 1;
+  while (a.S < 8 && tiles * a.S * 2 <= room && b.G >= a.S * 4) a.S *= 2;
+  a.b.P = (int)(a.S > 1 ? tiles * a.S : (tiles < room ? tiles : room));
+  return launched(launch_pdl_cl(kern, (unsigned)a.b.P, (unsigned)C::THREADS, (size_t)C::SMEM, s,
+                                (unsigned)a.S, mw, mx, a));
+}
+
+template <int DT>
+apex_status_t fb_dense_t(int64_t M, int64_t N, int64_t K, const void* a_codes, const void* w_codes,
+                         FBArgs a, bool early, cudaStream_t s) {
   const int sms = dev_info().sms;
+  CUtensorMap ma, mb;
+  if (!make_codes3_map(&mb, w_codes, 1, N, K, 128)) return APEX_ERR_CUDA;
+  if (M <= kSmallTokens) {
+    const int bt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    if (!make_expanded_map(&ma, a_codes, M, K, bt)) return APEX_ERR_CUDA;
+    a.tiles_m = (int)ceil_div(M, bt);
+    a.tiles_n = a.NB;
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (bt == 16) return launch_fs<16, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
+    if (bt == 32) return launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
+    return launch_fs<64, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
+  }
+  if (!make_expanded_map(&ma, a_codes, M, K, 128)) return APEX_ERR_CUDA;
+  a.tiles_m = (int)ceil_div(M, 128);
   const bool wide = (int64_t)a.tiles_m * ceil_div(N, 256) >= sms;
   a.tiles_n = (int)ceil_div(N, wide ? 256 : 128);
   const int64_t T = (int64_t)a.tiles_m * a.tiles_n;
   if (T >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
   a.P = (int)(T < sms ? T : sms);
+  return wide ? launch_fb<256, apex::FB_DENSE, DT>(ma, mb, a, s)
+              : launch_fb<128, apex::FB_DENSE, DT>(ma, mb, a, s);
+}
+
+// early: the activations' quantizer of the same call is the launch before this one.
+apex_status_t fb_dense(int64_t M, int64_t N, int64_t K, const void* a_codes, const void* a_scales,
+                       const void* w_codes, const void* w_scales, int32_t dtype, void* y,
+                       bool early, cudaStream_t s) {
+  FBArgs a = fb_args(M, N, K, a_scales, w_scales);
+  a.y = y;
+  a.y_vec = N % 8 == 0 && aligned(y, 16);
+  return dtype == APEX_DTYPE_F16 ? fb_dense_t<apex::DT_F16>(M, N, K, a_codes, w_codes, a, early, s)
+                                 : fb_dense_t<apex::DT_BF16>(M, N, K, a_codes, w_codes, a, early, s);
+}
+
+// FB_UP or FB_DOWN over the experts' rows, by the few-token kernel or the other one.  `rows`:
+// of the activations' codes; the launch before this one is the one that writes them.
+template <int KIND, int DT>
+apex_status_t fb_experts(const void* codes, int64_t rows, const void* w_codes, FBArgs a,
+                         cudaStream_t s) {
+  const int sms = dev_info().sms;
+  const int64_t S = a.slots, N = a.N, K = a.K;
   CUtensorMap ma, mb;
-  if (!make_expanded_map(&ma, a_codes, M, K, 128) || !make_codes3_map(&mb, w_codes, 1, N, K, 128))
+  if (!make_codes3_map(&mb, w_codes, (KIND == apex::FB_UP ? 2 : 1) * (int64_t)a.E, N, K, 128))
     return APEX_ERR_CUDA;
-  if (dtype == APEX_DTYPE_F16)
-    return wide ? launch_fb<256, apex::FB_DENSE, apex::DT_F16>(ma, mb, a, s)
-                : launch_fb<128, apex::FB_DENSE, apex::DT_F16>(ma, mb, a, s);
-  return wide ? launch_fb<256, apex::FB_DENSE, apex::DT_BF16>(ma, mb, a, s)
-              : launch_fb<128, apex::FB_DENSE, apex::DT_BF16>(ma, mb, a, s);
+  const int64_t experts = S < a.E ? S : a.E;
+  // at most: one partly filled tile for each expert that has rows, and the full ones
+  auto most_tiles = [&](int64_t bm, int64_t tiles_n) { return (experts + S / bm) * tiles_n; };
+  if (most_tiles(16, a.NB) >= (1ll << 31) - 8 * sms) return APEX_ERR_UNSUPPORTED;
+  if (S <= experts * kSmallRows) {
+    const int bt = S <= experts * 12 ? 16 : 32;
+    // FB_UP gathers single rows
+    if (!make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : bt)) return APEX_ERR_CUDA;
+    a.tiles_n = a.NB;
+    return bt == 16 ? launch_fs<16, KIND, DT>(mb, ma, a, most_tiles(16, a.NB), true, s)
+                    : launch_fs<32, KIND, DT>(mb, ma, a, most_tiles(32, a.NB), true, s);
+  }
+  if (!make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : 128)) return APEX_ERR_CUDA;
+  a.tiles_n = KIND == apex::FB_UP ? a.NB : (int)ceil_div(N, 256);
+  const int64_t tiles = most_tiles(128, a.tiles_n);
+  a.P = (int)(tiles < sms ? tiles : sms);
+  return launch_fb<256, KIND, DT>(ma, mb, a, s);
 }
 
 struct MoeWork {   // byte offsets into the workspace of apex_moe_mlp_fp8_block
@@ -296,7 +365,7 @@ apex_status_t apex_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* a
   if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(a_scales, 4) ||
       !aligned(w_scales, 4) || !aligned(y, 2))
     return APEX_ERR_ALIGNMENT;
-  return fb_dense(M, N, K, a_codes, a_scales, w_codes, w_scales, dtype, y,
+  return fb_dense(M, N, K, a_codes, a_scales, w_codes, w_scales, dtype, y, false,
                   static_cast<cudaStream_t>(stream));
 }
 
@@ -320,7 +389,8 @@ apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void*
   void* sc = ws + pad256((size_t)M * K);
   st = apex_quantize_act_fp8_block(x, dtype, M, K, ws, sc, stream);
   if (st != APEX_OK) return st;
-  return fb_dense(M, N, K, ws, sc, w_codes, w_scales, dtype, y, static_cast<cudaStream_t>(stream));
+  return fb_dense(M, N, K, ws, sc, w_codes, w_scales, dtype, y, true,
+                  static_cast<cudaStream_t>(stream));
 }
 
 apex_status_t apex_route_experts(const void* logits, int32_t dtype, int64_t T, int32_t E,
@@ -396,41 +466,26 @@ apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H,
   if (st != APEX_OK) return st;
 
   const int64_t S = T * k;
-  const int sms = dev_info().sms;
-  // at most: one partly filled tile for each expert that has rows, and the full ones
-  const int64_t most_tiles = (S < E ? S : (int64_t)E) + S / 128;
-  auto with_experts = [&](FBArgs a, int64_t tiles_n) {
+  auto with_experts = [&](FBArgs a) {
     a.E = E;
     a.slots = (int)S;
     a.top_k = k;
     a.offsets = static_cast<const int32_t*>(offsets_i32);
     a.order = static_cast<const int32_t*>(order_i32);
-    a.tiles_n = (int)tiles_n;
-    const int64_t tiles = most_tiles * tiles_n;
-    a.P = (int)(tiles < sms ? tiles : sms);
     return a;
   };
-  if (most_tiles * ceil_div(H > I ? H : I, 128) >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
-
-  CUtensorMap mx, mw13, mh, mw2;
-  if (!make_expanded_map(&mx, ws + w.xq, T, H, 1) ||
-      !make_codes3_map(&mw13, w13_codes, 2 * (int64_t)E, I, H, 128) ||
-      !make_expanded_map(&mh, ws + w.hq, S, I, 128) ||
-      !make_codes3_map(&mw2, w2_codes, E, H, I, 128))
-    return APEX_ERR_CUDA;
-
-  FBArgs up = with_experts(fb_args(T, I, H, ws + w.xs, w13_scales), ceil_div(I, 128));
+  FBArgs up = with_experts(fb_args(T, I, H, ws + w.xs, w13_scales));
   up.hq = ws + w.hq;
   up.hs = reinterpret_cast<float*>(ws + w.hs);
-  st = launch_fb<256, apex::FB_UP, apex::DT_BF16>(mx, mw13, up, s);
+  st = fb_experts<apex::FB_UP, apex::DT_BF16>(ws + w.xq, T, w13_codes, up, s);
   if (st != APEX_OK) return st;
 
-  FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales), ceil_div(H, 256));
+  FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales));
   down.y = ws + w.y;
   down.y_vec = 1;
   const bool f16 = dtype == APEX_DTYPE_F16;
-  st = f16 ? launch_fb<256, apex::FB_DOWN, apex::DT_F16>(mh, mw2, down, s)
-           : launch_fb<256, apex::FB_DOWN, apex::DT_BF16>(mh, mw2, down, s);
+  st = f16 ? fb_experts<apex::FB_DOWN, apex::DT_F16>(ws + w.hq, S, w2_codes, down, s)
+           : fb_experts<apex::FB_DOWN, apex::DT_BF16>(ws + w.hq, S, w2_codes, down, s);
   if (st != APEX_OK) return st;
 
   const unsigned blocks = grid_for(T * (H / 8), 256, 16);
