@@ -51,13 +51,23 @@ cudaError_t set_smem(F kern, int bytes, int* attr_dev) {   // once per device an
   return e;
 }
 
-template <int BN, int KIND, int DT>
-apex_status_t launch_fb(const CUtensorMap& ma, const CUtensorMap& mb, FBArgs a, cudaStream_t s) {
-  using C = FBCfg<BN>;
-  auto kern = apex::f8_block_gemm_kernel<BN, KIND, DT>;
+// Launches over `tiles` tiles (an upper bound for experts): one CTA, or pair of CTAs, per SM or
+// pair of SMs at most.
+template <int BN, int CG, int KIND, int DT>
+apex_status_t launch_fb(const void* a_codes, int64_t a_rows, const void* w_codes, int64_t Z,
+                        FBArgs a, int64_t tiles, cudaStream_t s) {
+  using C = FBCfg<BN, CG>;
+  auto kern = apex::f8_block_gemm_kernel<BN, CG, KIND, DT>;
   static thread_local int attr_dev = -1;
   if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
-  return launched(launch_pdl(kern, (unsigned)a.P, C::THREADS, (size_t)C::SMEM, s, ma, mb, a));
+  CUtensorMap ma, mb;
+  if (!make_expanded_map(&ma, a_codes, a_rows, a.K, 128) ||
+      !make_codes3_map(&mb, w_codes, Z, a.N, a.K, C::BOX))
+    return APEX_ERR_CUDA;
+  const int64_t most = dev_info().sms / CG;
+  a.P = (int)(tiles < most ? tiles : most) * CG;
+  return launched(launch_pdl_cl(kern, (unsigned)a.P, (unsigned)C::THREADS, (size_t)C::SMEM, s,
+                                (unsigned)CG, ma, mb, a));
 }
 
 template <int DT>
@@ -106,6 +116,8 @@ FBArgs fb_args(int64_t M, int64_t N, int64_t K, const void* sa, const void* sw) 
 // Up to this many tokens (dense), or rows of an expert on average, the few-token kernel runs.
 constexpr int64_t kSmallTokens = 128;
 constexpr int64_t kSmallRows = 48;
+// From this many rows of an expert on average, pairs of CTAs take 256 of them at once.
+constexpr int64_t kPairRows = 192;
 
 template <int BT, int KIND, int DT>
 apex_status_t launch_fs(const CUtensorMap& mw, const CUtensorMap& mx, const FBArgs& b,
@@ -130,11 +142,11 @@ template <int DT>
 apex_status_t fb_dense_t(int64_t M, int64_t N, int64_t K, const void* a_codes, const void* w_codes,
                          FBArgs a, bool early, cudaStream_t s) {
   const int sms = dev_info().sms;
-  CUtensorMap ma, mb;
-  if (!make_codes3_map(&mb, w_codes, 1, N, K, 128)) return APEX_ERR_CUDA;
   if (M <= kSmallTokens) {
     const int bt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    if (!make_expanded_map(&ma, a_codes, M, K, bt)) return APEX_ERR_CUDA;
+    CUtensorMap ma, mb;
+    if (!make_codes3_map(&mb, w_codes, 1, N, K, 128) || !make_expanded_map(&ma, a_codes, M, K, bt))
+      return APEX_ERR_CUDA;
     a.tiles_m = (int)ceil_div(M, bt);
     a.tiles_n = a.NB;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
@@ -142,15 +154,19 @@ apex_status_t fb_dense_t(int64_t M, int64_t N, int64_t K, const void* a_codes, c
     if (bt == 32) return launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
     return launch_fs<64, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
   }
-  if (!make_expanded_map(&ma, a_codes, M, K, 128)) return APEX_ERR_CUDA;
-  a.tiles_m = (int)ceil_div(M, 128);
-  const bool wide = (int64_t)a.tiles_m * ceil_div(N, 256) >= sms;
-  a.tiles_n = (int)ceil_div(N, wide ? 256 : 128);
-  const int64_t T = (int64_t)a.tiles_m * a.tiles_n;
-  if (T >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
-  a.P = (int)(T < sms ? T : sms);
-  return wide ? launch_fb<256, apex::FB_DENSE, DT>(ma, mb, a, s)
-              : launch_fb<128, apex::FB_DENSE, DT>(ma, mb, a, s);
+  if (ceil_div(M, 128) * ceil_div(N, 128) >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
+  // 256 x 256 by pairs of CTAs where their tiles fill the GPU, else 256 x 128, else 128 x 128
+  auto tiles = [&](int bm, int bn) {
+    a.tiles_m = (int)ceil_div(M, bm);
+    a.tiles_n = (int)ceil_div(N, bn);
+    return (int64_t)a.tiles_m * a.tiles_n;
+  };
+  if (int64_t t = tiles(256, 256); 2 * t >= sms)
+    return launch_fb<256, 2, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
+  if (int64_t t = tiles(256, 128); 4 * t >= sms && M > 128)
+    return launch_fb<128, 2, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
+  const int64_t t = tiles(128, 128);
+  return launch_fb<128, 1, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
 }
 
 // early: the activations' quantizer of the same call is the launch before this one.
@@ -164,44 +180,49 @@ apex_status_t fb_dense(int64_t M, int64_t N, int64_t K, const void* a_codes, con
                                  : fb_dense_t<apex::DT_BF16>(M, N, K, a_codes, w_codes, a, early, s);
 }
 
+// Few rows for each expert: the few-token kernel, which gathers FB_UP's rows of tokens itself.
+bool moe_small(int64_t S, int64_t E) { return S <= (S < E ? S : E) * kSmallRows; }
+
 // FB_UP or FB_DOWN over the experts' rows, by the few-token kernel or the other one.  `rows`:
 // of the activations' codes; the launch before this one is the one that writes them.
 template <int KIND, int DT>
 apex_status_t fb_experts(const void* codes, int64_t rows, const void* w_codes, FBArgs a,
                          cudaStream_t s) {
-  const int sms = dev_info().sms;
   const int64_t S = a.slots, N = a.N, K = a.K;
-  CUtensorMap ma, mb;
-  if (!make_codes3_map(&mb, w_codes, (KIND == apex::FB_UP ? 2 : 1) * (int64_t)a.E, N, K, 128))
-    return APEX_ERR_CUDA;
+  const int64_t Z = (KIND == apex::FB_UP ? 2 : 1) * (int64_t)a.E;
   const int64_t experts = S < a.E ? S : a.E;
   // at most: one partly filled tile for each expert that has rows, and the full ones
   auto most_tiles = [&](int64_t bm, int64_t tiles_n) { return (experts + S / bm) * tiles_n; };
-  if (most_tiles(16, a.NB) >= (1ll << 31) - 8 * sms) return APEX_ERR_UNSUPPORTED;
-  if (S <= experts * kSmallRows) {
+  if (most_tiles(16, a.NB) >= (1ll << 31) - 4096) return APEX_ERR_UNSUPPORTED;
+  if (moe_small(S, a.E)) {
     const int bt = S <= experts * 12 ? 16 : 32;
-    // FB_UP gathers single rows
-    if (!make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : bt)) return APEX_ERR_CUDA;
+    CUtensorMap ma, mb;
+    if (!make_codes3_map(&mb, w_codes, Z, N, K, 128) ||
+        !make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : bt))
+      return APEX_ERR_CUDA;
     a.tiles_n = a.NB;
     return bt == 16 ? launch_fs<16, KIND, DT>(mb, ma, a, most_tiles(16, a.NB), true, s)
                     : launch_fs<32, KIND, DT>(mb, ma, a, most_tiles(32, a.NB), true, s);
   }
-  if (!make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : 128)) return APEX_ERR_CUDA;
   a.tiles_n = KIND == apex::FB_UP ? a.NB : (int)ceil_div(N, 256);
-  const int64_t tiles = most_tiles(128, a.tiles_n);
-  a.P = (int)(tiles < sms ? tiles : sms);
-  return launch_fb<256, KIND, DT>(ma, mb, a, s);
+  // pairs of CTAs take 256 rows of an expert at once: not worth it under about that many
+  if (S >= experts * kPairRows)
+    return launch_fb<256, 2, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(256, a.tiles_n), s);
+  return launch_fb<256, 1, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(128, a.tiles_n), s);
 }
 
 struct MoeWork {   // byte offsets into the workspace of apex_moe_mlp_fp8_block
-  size_t xq, xs, hq, hs, y, total;
+  size_t xq, xs, pq, ps, hq, hs, y, total;
 };
-MoeWork moe_work(int64_t T, int64_t k, int64_t H, int64_t I) {
+MoeWork moe_work(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   MoeWork w;
   const size_t S = (size_t)T * (size_t)k;
   w.xq = 0;
   w.xs = w.xq + pad256((size_t)T * H);
-  w.hq = w.xs + pad256((size_t)T * ceil_div(H, 128) * 4);
+  w.pq = w.xs + pad256((size_t)T * ceil_div(H, 128) * 4);
+  // the tokens' rows by slot, where they are not gathered
+  w.ps = w.pq + (moe_small((int64_t)S, E) ? 0 : pad256(S * H));
+  w.hq = w.ps + (moe_small((int64_t)S, E) ? 0 : pad256(S * ceil_div(H, 128) * 4));
   w.hs = w.hq + pad256(S * I);
   w.y = w.hs + pad256(S * ceil_div(I, 128) * 4);
   w.total = w.y + pad256(S * H * 2);
@@ -437,7 +458,7 @@ apex_status_t apex_route_plan_experts(const void* logits, int32_t dtype, int64_t
 size_t apex_moe_mlp_fp8_block_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H,
                                              int64_t I) {
   if (check_moe(T, E, k, H, I) != APEX_OK) return 0;
-  return moe_work(T, k, H, I).total;
+  return moe_work(T, E, k, H, I).total;
 }
 
 apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
@@ -458,7 +479,7 @@ apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H,
       !aligned(offsets_i32, 4) || !aligned(order_i32, 4) || !aligned(w13_scales, 4) ||
       !aligned(w2_scales, 4))
     return APEX_ERR_ALIGNMENT;
-  const MoeWork w = moe_work(T, k, H, I);
+  const MoeWork w = moe_work(T, E, k, H, I);
   if (workspace_bytes < w.total) return APEX_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -474,10 +495,20 @@ apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H,
     a.order = static_cast<const int32_t*>(order_i32);
     return a;
   };
-  FBArgs up = with_experts(fb_args(T, I, H, ws + w.xs, w13_scales));
+  const bool small = moe_small(S, E);
+  if (!small) {
+    st = launched(launch_pdl(apex::f8_permute_kernel, grid_for(S * 32, 256, 8), 256, 0, s,
+                             (const uint8_t*)(ws + w.xq), (const float*)(ws + w.xs),
+                             static_cast<const int32_t*>(order_i32), (int)S, (int)k, (int)H,
+                             (int)ceil_div(H, 128), ws + w.pq,
+                             reinterpret_cast<float*>(ws + w.ps)));
+    if (st != APEX_OK) return st;
+  }
+  FBArgs up = with_experts(fb_args(small ? T : S, I, H, ws + (small ? w.xs : w.ps), w13_scales));
   up.hq = ws + w.hq;
   up.hs = reinterpret_cast<float*>(ws + w.hs);
-  st = fb_experts<apex::FB_UP, apex::DT_BF16>(ws + w.xq, T, w13_codes, up, s);
+  st = fb_experts<apex::FB_UP, apex::DT_BF16>(ws + (small ? w.xq : w.pq), small ? T : S, w13_codes,
+                                              up, s);
   if (st != APEX_OK) return st;
 
   FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales));

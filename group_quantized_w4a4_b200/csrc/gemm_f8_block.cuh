@@ -9,19 +9,27 @@
 //
 // Kinds:
 //   FB_DENSE  Y[M][N] = A . W^T.
-//   FB_UP     for rows grouped by expert (slots), row of slot s = token order[s] / k: the
-//             products with the expert's gate and up matrices, h = silu(gate) * up, quantized
-//             in groups of 128 as the next product's operand.  A tile is 128 rows x 128
-//             columns of h: its weight operand is 128 gate rows above 128 up rows.
+//   FB_UP     for rows grouped by expert (slots): the products with the expert's gate and up
+//             matrices, h = silu(gate) * up, quantized in groups of 128 as the next product's
+//             operand.  A tile is 128 columns of h: its weight operand is 128 gate rows above
+//             128 up rows.  The rows are slots: f8_permute_kernel has copied each token's
+//             codes to the slots of its choices (fetching scattered rows here by TMA gathers of
+//             four took 1.5 us a K-group, three times the products).
 //   FB_DOWN   h . W^T of each slot's expert, written to row order[s] (token-major).
-// FB_UP fetches its scattered token rows by TMA row gathers (four rows each), so no permuted
-// copy of the activations is made.
 //
 // Tile: 128 tokens (MMA M) x BN weight rows (MMA N), one K-group per pipeline stage, both
 // operands by TMA with 128-byte swizzle; the group's partial goes to one of 512 / BN
 // tensor-memory slots, which the epilogue drains while the next groups' MMAs fill the others.
-// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA, warps 4..11
-// epilogue (warp w: lanes 32*(w%4).., half (w-4)/4 of the columns).
+// CG = 2: the CTAs of a cluster of two compute 256 tokens x BN together (tcgen05
+// cta_group::2): each loads its own 128 tokens and half of the weight rows, which the tensor
+// cores read from both.  A 128 x 256 tile alone needs 48 KB of operands a K-group from L2, and
+// that stream (10.7 TB/s at 4096 x 8192 x 8192) is what bounded it; a pair needs 32 KB a CTA.
+// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA (of the even CTA),
+// warps 2, 3 scales (global memory to a ring in shared memory, four K-groups of the 128 tokens
+// and of the tile's two weight blocks at a time), warps 4..11 epilogue (warp w: lanes
+// 32*(w%4).., half (w-4)/4 of the columns).  With its 128 accumulators and 64 partials in
+// flight an epilogue thread has no registers for scales on their way from memory: loaded
+// there, every fourth group waited 1,100 cycles for them.
 #pragma once
 #include <cuda.h>
 #include <stdint.h>
@@ -54,27 +62,33 @@ struct FBArgs {
 
 constexpr int kMaxExperts = 512;
 
-template <int BN>
+template <int BN, int CG>
 struct FBCfg {
-  static constexpr int BM = 128;
-  static constexpr int A_BYTES = BM * 128;
-  static constexpr int B_BYTES = BN * 128;
+  static constexpr int BM = 128 * CG;              // rows of a tile, 128 of them in each CTA
+  static constexpr int BROWS = BN / CG;            // weight rows that a CTA loads
+  static constexpr int BOX = BROWS < 128 ? BROWS : 128;
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = BROWS * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int NS = BN == 256 ? 4 : 6;
+  static constexpr int NS = 168 * 1024 / STAGE;
   static constexpr int SLOTS = 512 / BN;
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  // 384 x 168 registers at launch; the first warpgroup keeps 40, the epilogue takes 232
-  static constexpr int REGS_CTRL = 40, REGS_EPI = 232;
+  // 384 x 168 registers at launch; the first warpgroup keeps 56, the epilogue takes 224
+  static constexpr int REGS_CTRL = 56, REGS_EPI = 224;
   static_assert(128 * REGS_CTRL + 256 * REGS_EPI <= THREADS * 168, "register pool");
   static constexpr int CPT = BN / 2;   // partials per epilogue thread
-  static constexpr int OFF_CUM = NS * STAGE;                       // [kMaxExperts + 1] ints
+  static constexpr int SR = 4;                     // ring of scale blocks (4 K-groups each)
+  static constexpr int SC_BLOCK = 4 * (128 + 2) * 4;               // [4][128] tokens, [4][2] weights
+  static constexpr int OFF_ST = NS * STAGE;        // 4 KB a warp: outputs on their way to rows
+  static constexpr int OFF_SC = OFF_ST + EPI_WARPS * 4096;
+  static constexpr int OFF_CUM = OFF_SC + SR * SC_BLOCK;           // [kMaxExperts + 1] ints
   static constexpr int OFF_AMAX = OFF_CUM + (kMaxExperts + 4) * 4;  // [2][2][128] words
   static constexpr int OFF_BAR = OFF_AMAX + 2 * 2 * 128 * 4;
-  static constexpr int NBAR = 2 * NS + 2 * SLOTS + 1;
+  static constexpr int NBAR = 2 * NS + 2 * SLOTS + 1 + 2 * SR;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(OFF_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory budget");
 };
 
 // The number of rows of expert e, clamped so that no offsets array leads out of the slots.
@@ -149,9 +163,6 @@ __device__ __forceinline__ float4 scales4(const float* row, int g0, int G, bool 
   return v;
 }
 
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
 __device__ __forceinline__ float at4(const float4& v, int j) {
   return j < 2 ? (j == 0 ? v.x : v.y) : (j == 2 ? v.z : v.w);
 }
@@ -160,12 +171,45 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-template <int BN, int KIND, int DT>
-__global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
+// Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k.
+// Bound: the copy itself, a byte read (from L2, k times) and written per element.  A warp per
+// slot.
+__global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restrict__ codes,
+                                                         const float* __restrict__ scales,
+                                                         const int32_t* __restrict__ order,
+                                                         int slots, int top_k, int K, int G,
+                                                         uint8_t* __restrict__ to_codes,
+                                                         float* __restrict__ to_scales) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int chunks = K / 16;
+  for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < slots; s += gridDim.x * 8) {
+    const int f = __ldg(order + s);
+    if (f < 0 || f >= slots) continue;   // no choice
+    const int t = f / top_k;
+    const uint4* src = reinterpret_cast<const uint4*>(codes + (size_t)t * K);
+    uint4* dst = reinterpret_cast<uint4*>(to_codes + (size_t)s * K);
+    for (int c0 = 0; c0 < chunks; c0 += 128) {   // four loads in flight
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 32 * i + lane < chunks) v[i] = __ldg(src + c0 + 32 * i + lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 32 * i + lane < chunks) dst[c0 + 32 * i + lane] = v[i];
+    }
+    for (int g = lane; g < G; g += 32) to_scales[(size_t)s * G + g] = __ldg(scales + (size_t)t * G + g);
+  }
+}
+
+template <int BN, int CG, int KIND, int DT>
+__global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     f8_block_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB, const FBArgs args) {
-  using C = FBCfg<BN>;
+  using C = FBCfg<BN, CG>;
   using D = DTraits<DT>;
+  constexpr bool PAIR = CG == 2;
   constexpr bool EXPERTS = KIND != FB_DENSE;
   static_assert(KIND != FB_UP || BN == 256, "gate and up halves of 128");
   extern __shared__ uint8_t smem_raw[];
@@ -179,6 +223,8 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
   uint64_t* tfull = empty + C::NS;       // slot holds a finished partial (commit)
   uint64_t* tempty = tfull + C::SLOTS;   // slot read out (one arrival per epilogue warp)
   uint64_t* mma_done = tempty + C::SLOTS;
+  uint64_t* sfull = mma_done + 1;        // scale block written (every scale thread)
+  uint64_t* sempty = sfull + C::SR;      // scale block read (one arrival per epilogue warp)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   int* s_abort = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
   int* s_never = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
@@ -187,6 +233,8 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint64_t lim = args.wait_ns;
   const int G = args.G;
+  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;   // CTA of the pair; the even one leads
+  const int t_first = (int)blockIdx.x / CG, t_step = args.P / CG;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
@@ -195,7 +243,11 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), C::EPI_WARPS);
+      mbar_init(smem_u32(&tempty[i]), CG * C::EPI_WARPS);
+    }
+    for (int i = 0; i < C::SR; ++i) {
+      mbar_init(smem_u32(&sfull[i]), 64);
+      mbar_init(smem_u32(&sempty[i]), C::EPI_WARPS);
     }
     mbar_init(smem_u32(mma_done), 1);
     *s_abort = 0;
@@ -205,8 +257,13 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(s_tmem), 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(s_tmem), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(s_tmem), 512);
+      tmem_relinquish();
+    }
   }
   if constexpr (EXPERTS) {
     grid_dep_wait();   // the offsets
@@ -214,6 +271,10 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {   // both CTAs' barriers and tensor memory exist
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
   grid_dep_launch();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(s_tmem);
@@ -242,80 +303,137 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
       if constexpr (!EXPERTS) grid_dep_wait();
       int it = 0, last = -1;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < T; t += args.P) {
+      for (int t = t_first; ok && t < T; t += t_step) {
         const ExpertTile x = tile_of(t);
-        int r[4] = {0, 0, 0, 0};   // FB_UP: the tokens of this lane's four rows
-        if constexpr (KIND == FB_UP) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int s = x.row0 + min(4 * lane + i, x.rows - 1);   // past the end: the last row
-            const int f = __ldg(args.order + s);
-            r[i] = f >= 0 && f < args.slots ? f / args.top_k : 0;
-          }
-        }
         for (int g = 0; g < G; ++g, ++it) {
           const int st = it % C::NS;
-          ok = mbar_wait(smem_u32(&empty[st]), ((uint32_t)(it / C::NS) & 1u) ^ 1u, lim, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = mbar_wait_warp(smem_u32(&empty[st]), ((uint32_t)(it / C::NS) & 1u) ^ 1u, lim, abort_flag);
           if (!ok) break;
-          const uint32_t fb = smem_u32(&full[st]);
+          // the bytes of both CTAs of a pair are counted on the even one's barrier
+          const uint32_t fb = PAIR ? cluster_map(smem_u32(&full[st]), 0u) : smem_u32(&full[st]);
           const uint32_t a_dst = smem_u32(smem + st * C::STAGE);
           const uint32_t b_dst = a_dst + C::A_BYTES;
-          if (lane == 0) mbar_arrive_expect_tx(fb, C::STAGE);
-          __syncwarp();
-          if constexpr (KIND == FB_UP) {
-            tma_gather4(a_dst + lane * 512, &tmA, fb, g * 128, r[0], r[1], r[2], r[3]);
-          }
-          if (lane == 0) {
-            if constexpr (KIND != FB_UP) tma_load_2d(a_dst, &tmA, fb, g * 128, x.row0);
-            if constexpr (KIND == FB_UP) {
-              tma_load_3d(b_dst, &tmB, fb, g * 128, x.tn * 128, 2 * x.e);
-              tma_load_3d(b_dst + 128 * 128, &tmB, fb, g * 128, x.tn * 128, 2 * x.e + 1);
-            } else {
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[st]), CG * C::STAGE);
+            if constexpr (PAIR) tma_load_2d_pair(a_dst, &tmA, fb, g * 128, x.row0 + 128 * rank);
+            else tma_load_2d(a_dst, &tmA, fb, g * 128, x.row0);
 #pragma unroll
-              for (int h = 0; h < BN / 128; ++h)
-                tma_load_3d(b_dst + h * 128 * 128, &tmB, fb, g * 128, x.tn * BN + h * 128, x.e);
+            for (int h = 0; h < C::BROWS / C::BOX; ++h) {
+              // FB_UP: 128 gate rows, then the 128 up rows of the same outputs
+              const int half = PAIR ? rank : h;
+              const int n = KIND == FB_UP ? x.tn * 128 : x.tn * BN + half * C::BOX;
+              const int z = KIND == FB_UP ? 2 * x.e + half : x.e;
+              if constexpr (PAIR) tma_load_3d_pair(b_dst + h * C::BOX * 128, &tmB, fb, g * 128, n, z);
+              else tma_load_3d(b_dst + h * C::BOX * 128, &tmB, fb, g * 128, n, z);
             }
           }
           __syncwarp();
           last = it;
         }
       }
-      // never leave the CTA with bulk copies in flight
-      for (int s = (last - C::NS + 1 > 0 ? last - C::NS + 1 : 0); s <= last; ++s)
-        mbar_wait(smem_u32(&full[s % C::NS]), (uint32_t)(s / C::NS) & 1u, lim, never);
+      // never leave the CTA with bulk copies in flight (the even CTA's barriers count the
+      // other's copies too, and the pair leaves together; the other CTA, after a wait that gave
+      // up, lets its last copies land)
+      if (rank == 0) {
+        for (int s = (last - C::NS + 1 > 0 ? last - C::NS + 1 : 0); s <= last; ++s)
+          mbar_wait(smem_u32(&full[s % C::NS]), (uint32_t)(s / C::NS) & 1u, lim, never);
+      } else if (!ok) {
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+      }
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc = idesc_e4m3(C::BM, BN);
       int it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < T; t += args.P) {
+      bool ok = rank == 0;
+      for (int t = t_first; ok && t < T; t += t_step) {
         for (int g = 0; g < G; ++g, ++it) {
           const int st = it % C::NS, sl = it % C::SLOTS;
-          ok = mbar_wait2(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
+          ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
                           ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t a_at = smem_u32(smem + st * C::STAGE);
             const uint64_t a0 = smem_desc_k_sw128(a_at);
             const uint64_t b0 = smem_desc_k_sw128(a_at + C::A_BYTES);
             const uint32_t d = tbase + sl * BN;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)   // 32 codes of K per MMA (+2 in 16-byte units)
-              umma_f8_ss(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
-            umma_commit(smem_u32(&empty[st]));
-            umma_commit(smem_u32(&tfull[sl]));
+            for (int j = 0; j < 4; ++j) {   // 32 codes of K per MMA (+2 in 16-byte units)
+              if constexpr (PAIR)
+                umma_f8_ss_pair(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
+              else
+                umma_f8_ss(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              umma_commit_pair(smem_u32(&empty[st]));
+              umma_commit_pair(smem_u32(&tfull[sl]));
+            } else {
+              umma_commit(smem_u32(&empty[st]));
+              umma_commit(smem_u32(&tfull[sl]));
+            }
           }
           __syncwarp();
         }
       }
-      if (lane == 0) umma_commit(smem_u32(mma_done));
+      if (elect_one() && rank == 0) {   // arrives in both CTAs of a pair
+        if constexpr (PAIR) umma_commit_pair(smem_u32(mma_done));
+        else umma_commit(smem_u32(mma_done));
+      }
       __syncwarp();
       mbar_wait(smem_u32(mma_done), 0u, lim, never);
       __syncwarp();
+    } else {
+      // ---------------------------------------------------------- scales
+      if constexpr (!EXPERTS) grid_dep_wait();
+      const int i0 = threadIdx.x - 64;          // rows i0 and i0 + 64 of this CTA's 128
+      const bool s_vec = args.s_vec != 0;
+      int sb = 0;
+      bool ok = true;
+      for (int t = t_first; ok && t < T; t += t_step) {
+        const ExpertTile x = tile_of(t);
+        const float* sa[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 128 * rank + i0 + 64 * i;
+          sa[i] = nullptr;
+          if (r < x.rows) sa[i] = args.sa + (size_t)(x.row0 + r) * G;
+        }
+        // the tile's weight blocks: of its two column halves, or FB_UP's gate and up (clamped:
+        // columns past N are not written)
+        const float* sw = nullptr;
+        if (i0 < 2) {
+          if constexpr (KIND == FB_UP) sw = args.sw + ((size_t)(2 * x.e + i0) * args.NB + x.tn) * G;
+          else sw = args.sw + ((size_t)x.e * args.NB + min((x.tn * BN + i0 * C::CPT) / 128, args.NB - 1)) * G;
+        }
+        for (int gb = 0; gb < G; gb += 4, ++sb) {
+          const int b = sb % C::SR;
+          float4 v[2], w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            v[i] = sa[i] ? scales4(sa[i], gb, G, s_vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (sw) w = scales4(sw, gb, G, s_vec);
+          ok = mbar_wait_warp(smem_u32(&sempty[b]), ((uint32_t)(sb / C::SR) & 1u) ^ 1u, lim, abort_flag);
+          if (!ok) break;
+          float* blk = reinterpret_cast<float*>(smem + C::OFF_SC + b * C::SC_BLOCK);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float* d = blk + i0 + 64 * i;
+            d[0] = v[i].x;
+            d[128] = v[i].y;
+            d[256] = v[i].z;
+            d[384] = v[i].w;
+          }
+          if (i0 < 2) {
+            float* d = blk + 512 + i0;
+            d[0] = w.x;
+            d[2] = w.y;
+            d[4] = w.z;
+            d[6] = w.w;
+          }
+          mbar_arrive(smem_u32(&sfull[b]));
+        }
+      }
     }
   } else {
     regs_inc<C::REGS_EPI>();
@@ -323,9 +441,9 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     if constexpr (!EXPERTS) grid_dep_wait();
     const int lq = warp & 3;                  // tensor-memory lane quarter of this warp
     const int half = (warp - 4) >> 2;
-    const int row = 32 * lq + lane;           // token of the tile
+    const int row = 32 * lq + lane;           // token of this CTA's 128
+    const int trow = 128 * rank + row;        // token of the tile
     const uint32_t t_lane = (uint32_t)(32 * lq) << 16;
-    const bool s_vec = args.s_vec != 0;
     constexpr int NCH = C::CPT / 32;
     // tensor-memory column of this thread's 32-column chunk cc: for FB_UP its 64 gate
     // columns, then the 64 up columns of the same outputs
@@ -335,67 +453,84 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     };
     float2 acc[C::CPT / 2];
     bool ok = true;
-    int it = 0;
+    int it = 0, sb = 0;
     uint32_t par = 0;
-    for (int t = blockIdx.x; ok && t < T; t += args.P, par ^= 1u) {
+    for (int t = t_first; ok && t < T; t += t_step, par ^= 1u) {
       const ExpertTile x = tile_of(t);
-      const bool live = row < x.rows;
-      const int s = x.row0 + (live ? row : 0);
-      int f = 0;   // this row's flat (token, choice) index
-      if constexpr (EXPERTS) {
-        f = __ldg(args.order + s);
-        if (f < 0 || f >= args.slots) f = -1;
+      const bool live = trow < x.rows;
+      const int s = x.row0 + (live ? trow : 0);
+      int out_row = live ? s : -1;
+      if constexpr (KIND == FB_DOWN) {
+        if (live) {
+          out_row = __ldg(args.order + s);
+          if (out_row >= args.slots) out_row = -1;
+        }
       }
-      const int a_row = KIND == FB_UP ? (f < 0 ? 0 : f / args.top_k) : s;
-      const float* sa = args.sa + (size_t)a_row * G;
-      // the weight blocks of this thread's columns (clamped: columns past N are not written)
-      const int nb0 = KIND == FB_UP ? x.tn : min((x.tn * BN + half * C::CPT) / 128, args.NB - 1);
-      const float* sw0 = args.sw + ((size_t)(KIND == FB_UP ? 2 * x.e : x.e) * args.NB + nb0) * G;
-      const float* sw1 = sw0 + (size_t)args.NB * G;   // FB_UP: the up matrix
 #pragma unroll
       for (int e = 0; e < C::CPT / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
-      float4 sa_n = scales4(sa, 0, G, s_vec), w0_n = scales4(sw0, 0, G, s_vec), w1_n = w0_n;
-      if constexpr (KIND == FB_UP) w1_n = scales4(sw1, 0, G, s_vec);
-      for (int gb = 0; ok && gb < G; gb += 4) {
-        const float4 c0 = mul4(sa_n, w0_n);
-        const float4 c1 = KIND == FB_UP ? mul4(sa_n, w1_n) : c0;
-        if (gb + 4 < G) {   // the next four groups' scales are in flight meanwhile
-          sa_n = scales4(sa, gb + 4, G, s_vec);
-          w0_n = scales4(sw0, gb + 4, G, s_vec);
-          if constexpr (KIND == FB_UP) w1_n = scales4(sw1, gb + 4, G, s_vec);
-        }
-        const int je = min(4, G - gb);
-        for (int j = 0; j < je; ++j, ++it) {
-          const int sl = it % C::SLOTS;
-          ok = mbar_wait(smem_u32(&tfull[sl]), (uint32_t)(it / C::SLOTS) & 1u, lim, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t td = tbase + t_lane + sl * BN;
-          const float k0 = at4(c0, j), k1 = at4(c1, j);
-          uint32_t p[2][32];
-          tmem_ld32_nowait(td + chunk_col(0), p[0]);
-          tmem_ld_wait32(p[0]);
+      // A flat pipeline of 32-column chunks: each one's load is issued a chunk ahead, across
+      // groups too, so that only the first of a tile waits for its latency (about 220 cycles)
+      uint32_t p[2][32];
+      auto wait_block = [&]() {
+        return mbar_wait_warp(smem_u32(&sfull[sb % C::SR]), (uint32_t)(sb / C::SR) & 1u, lim, abort_flag);
+      };
+      auto load_first = [&]() {   // waits for group `it` and starts its first chunk
+        if (!mbar_wait_warp(smem_u32(&tfull[it % C::SLOTS]), (uint32_t)(it / C::SLOTS) & 1u, lim, abort_flag))
+          return false;
+        tc_fence_after();
+        tmem_ld32_nowait(tbase + t_lane + (it % C::SLOTS) * BN + chunk_col(0), p[0]);
+        return true;
+      };
+      auto done_block = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[sb % C::SR]));
+        ++sb;
+      };
+      ok = wait_block() && load_first();
+      for (int g = 0; ok && g < G; ++g) {
+        const int sl = it % C::SLOTS;
+        const uint32_t td = tbase + t_lane + sl * BN;
+        const float* blk = reinterpret_cast<const float*>(smem + C::OFF_SC + (sb % C::SR) * C::SC_BLOCK);
+        const int j = g & 3;
+        const float a_s = blk[j * 128 + row];
+        const float k0 = a_s * blk[512 + j * 2 + (KIND == FB_UP ? 0 : half)];
+        const float k1 = KIND == FB_UP ? a_s * blk[512 + j * 2 + 1] : k0;
 #pragma unroll
-          for (int cc = 0; cc < NCH; ++cc) {
-            uint32_t* pc = p[cc & 1];
-            if (cc + 1 < NCH) tmem_ld32_nowait(td + chunk_col(cc + 1), p[(cc + 1) & 1]);
-            const float kk = KIND == FB_UP && cc >= 2 ? k1 : k0;
-            const float2 k2 = make_float2(kk, kk);
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              acc[cc * 16 + q] = __ffma2_rn(
-                  make_float2(__uint_as_float(pc[2 * q]), __uint_as_float(pc[2 * q + 1])), k2,
-                  acc[cc * 16 + q]);
-            if (cc + 1 < NCH) tmem_ld_wait32(p[(cc + 1) & 1]);
-            if (cc == NCH - 2) {   // every load of the slot has completed
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&tempty[sl]));
+        for (int cc = 0; cc < NCH; ++cc) {
+          uint32_t* pc = p[cc & 1];
+          tmem_ld_wait32(pc);
+          if (cc + 1 < NCH) {
+            tmem_ld32_nowait(td + chunk_col(cc + 1), p[(cc + 1) & 1]);
+          } else {   // every load of the slot has completed
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster(cluster_map(smem_u32(&tempty[sl]), 0u));
+              else mbar_arrive(smem_u32(&tempty[sl]));
+            }
+            ++it;
+            if (g + 1 < G) {
+              if (j == 3) {
+                done_block();
+                ok = wait_block();
+              }
+              ok = ok && load_first();
             }
           }
+          const float kk = KIND == FB_UP && cc >= 2 ? k1 : k0;
+          const float2 k2 = make_float2(kk, kk);
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            acc[cc * 16 + q] = __ffma2_rn(
+                make_float2(__uint_as_float(pc[2 * q]), __uint_as_float(pc[2 * q + 1])), k2,
+                acc[cc * 16 + q]);
         }
       }
+      done_block();
+      // The tile's outputs go through the warp's own 4 KB of shared memory (16-byte chunks,
+      // permuted so that neither side meets bank conflicts), so that a store writes whole
+      // 128-byte (FB_UP: 64-byte) lines of a few rows instead of 16 bytes of 32 rows.
+      uint8_t* stage = smem + C::OFF_ST + (warp - 4) * 4096;
       if constexpr (KIND == FB_UP) {
         // h of this thread's 64 columns, the group's maximum with the thread that holds the
         // row's other 64, then the codes
@@ -412,43 +547,64 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
         uint32_t* am = s_amax + par * 256;
         am[half * 128 + row] = mx;
         ok = !bar_red_or(1, 256, !ok);   // one decision for all epilogue warps
-        if (ok && live) {
+        if (ok) {
           mx = max(mx, am[(half ^ 1) * 128 + row]);
           const F8Scale q = f8_scale(mx);
-          uint8_t* dst = args.hq + (size_t)s * args.N + n0;
 #pragma unroll
-          for (int e = 0; e < 64; e += 16) {   // N % 16 == 0
-            if (n0 + e < args.N) {
-              float v0[8], v1[8];
+          for (int e = 0; e < 64; e += 16) {
+            float v0[8], v1[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                v0[i] = h[e + i];
-                v1[i] = h[e + 8 + i];
-              }
-              const uint2 a = f8_codes8(v0, q), b = f8_codes8(v1, q);
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(a.x, a.y, b.x, b.y);
+            for (int i = 0; i < 8; ++i) {
+              v0[i] = h[e + i];
+              v1[i] = h[e + 8 + i];
             }
+            const uint2 a = f8_codes8(v0, q), b = f8_codes8(v1, q);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + (((e >> 4) ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(a.x, a.y, b.x, b.y);
           }
-          if (half == 0) args.hs[(size_t)s * args.NB + x.tn] = q.s;
+          if (half == 0 && live) args.hs[(size_t)s * args.NB + x.tn] = q.s;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), c = lane & 3;
+            const int slot = __shfl_sync(0xffffffffu, out_row, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            if (slot >= 0 && n0 + c * 16 < args.N)   // N % 16 == 0
+              *reinterpret_cast<uint4*>(args.hq + (size_t)slot * args.N + n0 + c * 16) = v;
+          }
+          __syncwarp();
         }
-      } else {
-        const int n0 = x.tn * BN + half * C::CPT;
-        const int out_row = KIND == FB_DOWN ? f : s;
-        if (ok && live && out_row >= 0) {
-          typename D::T* dst = static_cast<typename D::T*>(args.y) + (size_t)out_row * args.N + n0;
-          if (args.y_vec && n0 + C::CPT <= args.N) {
+      } else if (ok) {
 #pragma unroll
-            for (int e = 0; e < C::CPT / 2; e += 4)
-              *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(
-                  D::pack(acc[e].x, acc[e].y), D::pack(acc[e + 1].x, acc[e + 1].y),
-                  D::pack(acc[e + 2].x, acc[e + 2].y), D::pack(acc[e + 3].x, acc[e + 3].y));
-          } else {
+        for (int pass = 0; pass < C::CPT / 64; ++pass) {
 #pragma unroll
-            for (int e = 0; e < C::CPT; ++e) {
-              const float v = (e & 1) ? acc[e / 2].y : acc[e / 2].x;
-              if (n0 + e < args.N) dst[e] = D::one(v);
+          for (int c = 0; c < 8; ++c) {
+            const float2* a = acc + pass * 32 + c * 4;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(D::pack(a[0].x, a[0].y), D::pack(a[1].x, a[1].y),
+                           D::pack(a[2].x, a[2].y), D::pack(a[3].x, a[3].y));
+          }
+          __syncwarp();
+          const int n = x.tn * BN + half * C::CPT + pass * 64 + (lane & 7) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const int to = __shfl_sync(0xffffffffu, out_row, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (to < 0) continue;
+            typename D::T* dst = static_cast<typename D::T*>(args.y) + (size_t)to * args.N + n;
+            if (args.y_vec) {   // N % 8 == 0
+              if (n < args.N) *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (n + e < args.N)
+                  reinterpret_cast<uint16_t*>(dst)[e] =
+                      (uint16_t)((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
             }
           }
+          __syncwarp();
         }
       }
     }
@@ -456,9 +612,14 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) {   // neither CTA's memory is in use by the other any more
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tbase, 512);
+    else tmem_dealloc(tbase, 512);
   }
 }
 

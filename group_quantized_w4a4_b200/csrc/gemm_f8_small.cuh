@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
     if (fs.early && t_first < T) {
       const ExpertTile x = tile_of(t_first);
       pre = min(C::NS, units);
-      if (lane == 0) {
+      if (elect_one()) {
         for (int u = 0; u < pre; ++u) {
           mbar_arrive_expect_tx(smem_u32(&full[u]), C::STAGE);
           load_w(x, u, u);
@@ -200,13 +200,12 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
       }
       for (int u = 0; u < units; ++u, ++it) {
         const int st = it % C::NS;
-        ok = mbar_wait(smem_u32(&empty[st]), ((uint32_t)(it / C::NS) & 1u) ^ 1u, lim, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = mbar_wait_warp(smem_u32(&empty[st]), ((uint32_t)(it / C::NS) & 1u) ^ 1u, lim, abort_flag);
         if (!ok) break;
         const uint32_t fb = smem_u32(&full[st]);
         const uint32_t x_dst = smem_u32(smem + st * C::STAGE + C::W_BYTES);
         const int g = g0 + u / HALVES;
-        if (lane == 0 && it >= pre) {
+        if (elect_one() && it >= pre) {
           mbar_arrive_expect_tx(fb, C::STAGE);
           load_w(x, u, st);
         }
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
           if (lane < BT / 4)
             tma_gather4(x_dst + lane * 512, &tmX, fb, g * 128, r[0], r[1], r[2], r[3]);
         } else {
-          if (lane == 0) tma_load_2d(x_dst, &tmX, fb, g * 128, x.row0);
+          if (elect_one()) tma_load_2d(x_dst, &tmX, fb, g * 128, x.row0);
         }
         __syncwarp();
         last = it;
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
     // whose weights alone were fetched, after a wait that gave up, cannot complete: its tokens
     // are fetched now)
     for (int it2 = last + 1; it2 < pre; ++it2) {
-      if (lane == 0 && KIND != FB_UP)
+      if (elect_one() && KIND != FB_UP)
         tma_load_2d(smem_u32(smem + it2 * C::STAGE + C::W_BYTES), &tmX, smem_u32(&full[it2]), 0, 0);
       if (KIND == FB_UP && lane < BT / 4)
         tma_gather4(smem_u32(smem + it2 * C::STAGE + C::W_BYTES) + lane * 512, &tmX,
@@ -243,12 +242,11 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
     for (int t = t_first; ok && t < T; t += t_step) {
       for (int u = 0; u < units; ++u, ++it) {
         const int st = it % C::NS, sl = it % C::SLOTS;
-        ok = mbar_wait2(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
+        ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
                         ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t at = smem_u32(smem + st * C::STAGE);
           const uint64_t w0 = smem_desc_k_sw128(at);
           const uint64_t x0 = smem_desc_k_sw128(at + C::W_BYTES);
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
         __syncwarp();
       }
     }
-    if (lane == 0) umma_commit(smem_u32(mma_done));
+    if (elect_one()) umma_commit(smem_u32(mma_done));
     __syncwarp();
     mbar_wait(smem_u32(mma_done), 0u, lim, never);
     __syncwarp();
