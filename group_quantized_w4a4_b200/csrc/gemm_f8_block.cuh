@@ -79,7 +79,7 @@ struct FBCfg {
   static_assert(128 * REGS_CTRL + 256 * REGS_EPI <= THREADS * 168, "register pool");
   static constexpr int CPT = BN / 2;   // partials per epilogue thread
   static constexpr int SR = 4;                     // ring of scale blocks (4 K-groups each)
-  static constexpr int SC_BLOCK = 4 * (128 + 2) * 4;               // [4][128] tokens, [4][2] weights
+  static constexpr int SC_BLOCK = (128 + 2) * 16;  // [128 tokens, 2 weight blocks][4 groups]
   static constexpr int OFF_ST = NS * STAGE;        // 4 KB a warp: outputs on their way to rows
   static constexpr int OFF_SC = OFF_ST + EPI_WARPS * 4096;
   static constexpr int OFF_CUM = OFF_SC + SR * SC_BLOCK;           // [kMaxExperts + 1] ints
@@ -349,8 +349,9 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
       for (int t = t_first; ok && t < T; t += t_step) {
         for (int g = 0; g < G; ++g, ++it) {
           const int st = it % C::NS, sl = it % C::SLOTS;
-          ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
-                          ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim, abort_flag);
+          ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u,
+                               smem_u32(&tempty[sl]), ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim,
+                               abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -415,22 +416,10 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
           if (sw) w = scales4(sw, gb, G, s_vec);
           ok = mbar_wait_warp(smem_u32(&sempty[b]), ((uint32_t)(sb / C::SR) & 1u) ^ 1u, lim, abort_flag);
           if (!ok) break;
-          float* blk = reinterpret_cast<float*>(smem + C::OFF_SC + b * C::SC_BLOCK);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float* d = blk + i0 + 64 * i;
-            d[0] = v[i].x;
-            d[128] = v[i].y;
-            d[256] = v[i].z;
-            d[384] = v[i].w;
-          }
-          if (i0 < 2) {
-            float* d = blk + 512 + i0;
-            d[0] = w.x;
-            d[2] = w.y;
-            d[4] = w.z;
-            d[6] = w.w;
-          }
+          float4* blk = reinterpret_cast<float4*>(smem + C::OFF_SC + b * C::SC_BLOCK);
+          blk[i0] = v[0];
+          blk[i0 + 64] = v[1];
+          if (i0 < 2) blk[128 + i0] = w;
           mbar_arrive(smem_u32(&sfull[b]));
         }
       }
@@ -468,55 +457,42 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
       }
 #pragma unroll
       for (int e = 0; e < C::CPT / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
-      // A flat pipeline of 32-column chunks: each one's load is issued a chunk ahead, across
-      // groups too, so that only the first of a tile waits for its latency (about 220 cycles)
+      // The partials come in chunks of 32 columns, the next one's load in flight while one is
+      // used.  (Asking for the next group's first chunk before this group's last fmas was
+      // slower, 0.54 against 0.45 us a K-group, and so was handing the slot back by a
+      // predicated arrive of the whole warp instead of one elected lane's, 0.56 us.)
       uint32_t p[2][32];
-      auto wait_block = [&]() {
-        return mbar_wait_warp(smem_u32(&sfull[sb % C::SR]), (uint32_t)(sb / C::SR) & 1u, lim, abort_flag);
-      };
-      auto load_first = [&]() {   // waits for group `it` and starts its first chunk
-        if (!mbar_wait_warp(smem_u32(&tfull[it % C::SLOTS]), (uint32_t)(it / C::SLOTS) & 1u, lim, abort_flag))
-          return false;
-        tc_fence_after();
-        tmem_ld32_nowait(tbase + t_lane + (it % C::SLOTS) * BN + chunk_col(0), p[0]);
-        return true;
-      };
-      auto done_block = [&]() {
+      float4 c0, c1;   // sa * sw of the four groups of the block (FB_UP: c1 of the up matrix)
+      auto block_bar = [&]() { return smem_u32(&sfull[sb % C::SR]); };
+      auto block_par = [&]() { return (uint32_t)(sb / C::SR) & 1u; };
+      auto load_block = [&]() {
+        const float4* blk = reinterpret_cast<const float4*>(smem + C::OFF_SC + (sb % C::SR) * C::SC_BLOCK);
+        const float4 a = blk[row], w0 = blk[128 + (KIND == FB_UP ? 0 : half)];
+        c0 = make_float4(a.x * w0.x, a.y * w0.y, a.z * w0.z, a.w * w0.w);
+        if constexpr (KIND == FB_UP) {
+          const float4 w1 = blk[129];
+          c1 = make_float4(a.x * w1.x, a.y * w1.y, a.z * w1.z, a.w * w1.w);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sempty[sb % C::SR]));
+        if (elect_one()) mbar_arrive(smem_u32(&sempty[sb % C::SR]));
         ++sb;
       };
-      ok = wait_block() && load_first();
+      auto load_chunk = [&](int i, int cc) {   // group number i's chunk cc
+        tmem_ld32_nowait(tbase + t_lane + (i % C::SLOTS) * BN + chunk_col(cc), p[cc & 1]);
+      };
+      auto wait_group = [&]() {
+        const bool r = mbar_wait_warp(smem_u32(&tfull[it % C::SLOTS]), (uint32_t)(it / C::SLOTS) & 1u, lim, abort_flag);
+        tc_fence_after();
+        return r;
+      };
+      ok = mbar_wait_warp(block_bar(), block_par(), lim, abort_flag);
+      if (ok) load_block();
       for (int g = 0; ok && g < G; ++g) {
         const int sl = it % C::SLOTS;
-        const uint32_t td = tbase + t_lane + sl * BN;
-        const float* blk = reinterpret_cast<const float*>(smem + C::OFF_SC + (sb % C::SR) * C::SC_BLOCK);
         const int j = g & 3;
-        const float a_s = blk[j * 128 + row];
-        const float k0 = a_s * blk[512 + j * 2 + (KIND == FB_UP ? 0 : half)];
-        const float k1 = KIND == FB_UP ? a_s * blk[512 + j * 2 + 1] : k0;
-#pragma unroll
-        for (int cc = 0; cc < NCH; ++cc) {
-          uint32_t* pc = p[cc & 1];
-          tmem_ld_wait32(pc);
-          if (cc + 1 < NCH) {
-            tmem_ld32_nowait(td + chunk_col(cc + 1), p[(cc + 1) & 1]);
-          } else {   // every load of the slot has completed
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR) mbar_arrive_cluster(cluster_map(smem_u32(&tempty[sl]), 0u));
-              else mbar_arrive(smem_u32(&tempty[sl]));
-            }
-            ++it;
-            if (g + 1 < G) {
-              if (j == 3) {
-                done_block();
-                ok = wait_block();
-              }
-              ok = ok && load_first();
-            }
-          }
+        const float k0 = at4(c0, j), k1 = KIND == FB_UP ? at4(c1, j) : k0;
+        auto fma_chunk = [&](int cc) {
+          const uint32_t* pc = p[cc & 1];
           const float kk = KIND == FB_UP && cc >= 2 ? k1 : k0;
           const float2 k2 = make_float2(kk, kk);
 #pragma unroll
@@ -524,9 +500,31 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
             acc[cc * 16 + q] = __ffma2_rn(
                 make_float2(__uint_as_float(pc[2 * q]), __uint_as_float(pc[2 * q + 1])), k2,
                 acc[cc * 16 + q]);
+        };
+        ok = wait_group();
+        if (!ok) break;
+        load_chunk(it, 0);
+        tmem_ld_wait32(p[0]);
+#pragma unroll
+        for (int cc = 0; cc < NCH; ++cc) {
+          if (cc + 1 < NCH) load_chunk(it, cc + 1);
+          fma_chunk(cc);
+          if (cc + 1 < NCH) tmem_ld_wait32(p[(cc + 1) & 1]);
+          if (cc == NCH - 2) {   // every load of the slot has completed
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) {
+              if constexpr (PAIR) mbar_arrive_cluster(cluster_map(smem_u32(&tempty[sl]), 0u));
+              else mbar_arrive(smem_u32(&tempty[sl]));
+            }
+          }
+        }
+        ++it;
+        if (j == 3 && g + 1 < G) {
+          ok = mbar_wait_warp(block_bar(), block_par(), lim, abort_flag);
+          if (ok) load_block();
         }
       }
-      done_block();
       // The tile's outputs go through the warp's own 4 KB of shared memory (16-byte chunks,
       // permuted so that neither side meets bank conflicts), so that a store writes whole
       // 128-byte (FB_UP: 64-byte) lines of a few rows instead of 16 bytes of 32 rows.

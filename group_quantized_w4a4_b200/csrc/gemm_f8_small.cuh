@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
       for (int u = 0; u < units; ++u, ++it) {
         const int st = it % C::NS, sl = it % C::SLOTS;
         ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u, smem_u32(&tempty[sl]),
-                        ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim, abort_flag);
+                             ((uint32_t)(it / C::SLOTS) & 1u) ^ 1u, lim, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {

@@ -303,7 +303,8 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, 
 }
 // Arrive at a barrier of another CTA of the cluster (rbar: a shared::cluster address), to hand
 // over tensor memory (tc_fence_before orders its reads): no ordinary memory is published, so
-// the arrive does not release at cluster scope.
+// the arrive does not release at cluster scope, which would wait for every earlier access of
+// the thread (569 instead of 338 us at 4096 x 8192 x 8192).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t rbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(rbar) : "memory");
 }
