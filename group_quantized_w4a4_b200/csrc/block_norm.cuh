@@ -40,26 +40,54 @@ __device__ __forceinline__ float block_sum(float v, float* s_part, int warps) {
   return t;
 }
 
+// 8 consecutive 16-bit elements as they are stored, and as fp32.
+__device__ __forceinline__ uint4 raw8(const void* base, size_t at) {
+  return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = DTraits<DT>::unpack(u[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+  return make_uint4(DTraits<DT>::pack(v[0], v[1]), DTraits<DT>::pack(v[2], v[3]),
+                    DTraits<DT>::pack(v[4], v[5]), DTraits<DT>::pack(v[6], v[7]));
+}
+
 // One CTA per token; thread i holds chunks i, i + blockDim, ... of 8 elements in registers, so
-// every tensor is read and written once.
-template <int DT, int NC>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a) {
+// every tensor is read and written once.  Bound: HBM for many tokens (x and residual in; h, y
+// and codes out), latency for a few.  A few tokens take one chunk a thread, the shortest chain;
+// many take four, in CTAs of 256 threads (at H = 8192), several of which share an SM, so that
+// one's loads cover the other's reductions.
+template <int DT, int NC, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const NormArgs a) {
   using D = DTraits<DT>;
   __shared__ float s_part[2][32];
   grid_dep_wait();
   grid_dep_launch();
   const int warps = blockDim.x >> 5;
   const size_t base = (size_t)blockIdx.x * a.H;
-  float z[NC][8];
-  bool in[NC];
-  float ss = 0.0f;
+  uint4 xr[NC], rr[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
-    in[i] = c < a.H;
+    xr[i] = rr[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < a.H) {
+      xr[i] = raw8(a.x, base + c);
+      if (a.residual) rr[i] = raw8(a.residual, base + c);
+    }
+  }
+  float z[NC][8];
+  float ss = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[i][j] = 0.0f;
-    if (in[i]) load8<DT>(a.x, base + c, z[i]);
+  for (int i = 0; i < NC; ++i) {
+    widen8<DT>(xr[i], z[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(z[i][j], z[i][j], ss);
   }
@@ -70,53 +98,42 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a) {
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
-    if (!in[i]) continue;
+    if (c >= a.H) continue;
+    float w[8];
     if (a.post) {
-      float w[8];
-      load8<DT>(a.post, c, w);
+      widen8<DT>(raw8(a.post, c), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * rs * (a.off + w[j]);
     }
     if (a.gate) {
-      float w[8];
-      load8<DT>(a.gate, gbase + c, w);
+      widen8<DT>(raw8(a.gate, gbase + c), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] *= w[j];
     }
-    if (a.residual) {
-      float w[8];
-      load8<DT>(a.residual, base + c, w);
+    widen8<DT>(rr[i], w);   // 0 without a residual
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] = fmaf(a.alpha, z[i][j], w[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] *= a.alpha;
+    for (int j = 0; j < 8; ++j) {
+      z[i][j] = fmaf(a.alpha, z[i][j], w[j]);
+      ss = fmaf(z[i][j], z[i][j], ss);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(z[i][j], z[i][j], ss);
-    if (a.h)
-      *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.h) + base + c) =
-          make_uint4(D::pack(z[i][0], z[i][1]), D::pack(z[i][2], z[i][3]),
-                     D::pack(z[i][4], z[i][5]), D::pack(z[i][6], z[i][7]));
+    if (a.h) *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.h) + base + c) = narrow8<DT>(z[i]);
   }
   if (!a.pre) return;
   rs = __frsqrt_rn(block_sum(ss, s_part[1], warps) / (float)a.H + a.eps);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
-    if (in[i]) {
+    const bool in = c < a.H;
+    if (in) {
       float w[8];
-      load8<DT>(a.pre, c, w);
+      widen8<DT>(raw8(a.pre, c), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * rs * (a.off + w[j]);
-      if (a.y)
-        *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.y) + base + c) =
-            make_uint4(D::pack(z[i][0], z[i][1]), D::pack(z[i][2], z[i][3]),
-                       D::pack(z[i][4], z[i][5]), D::pack(z[i][6], z[i][7]));
+      if (a.y) *reinterpret_cast<uint4*>(static_cast<typename D::T*>(a.y) + base + c) = narrow8<DT>(z[i]);
     }
     if (a.codes) {   // 16 lanes hold one group (the shuffles are warp-wide)
       const F8Scale q = f8_scale(half_warp_max(absmax8_bits(z[i])));
-      if (in[i]) {
+      if (in) {
         *reinterpret_cast<uint2*>(a.codes + base + c) = f8_codes8(z[i], q);
         if ((threadIdx.x & 15) == 0) a.scales[(size_t)blockIdx.x * a.G + c / 128] = q.s;
       }

@@ -5,11 +5,13 @@
 //   s = fp32_rne(a / 448)                      (IEEE fp32 division; 448 is E4M3's maximum)
 //   q = E4M3(x / s), the exact quotient rounded once, half to even (q = 0 when s == 0)
 // A NaN in the group makes s and every q NaN; an infinity makes s infinite (a NaN once
-// multiplied).  The exact quotient, not its fp32 rounding, decides: t = fl(x * fl(1/s)) is
-// within 1.5 ulp of it, so unless t lies within 4 ulp of the middle between two E4M3 values
-// both round alike; there the quotient is formed in 64 bits and rounded to odd in fp32, which
-// keeps it on its side of the middle (x has at most 24 significant bits, middle * s at most
-// 29, so their difference is 0 or far above a 64-bit quotient's error).
+// multiplied).  The exact quotient, not its fp32 rounding, decides: t = fl(x * r), r within an
+// ulp of 1/s, is within 3 ulp of it, so unless t lies within 4 ulp of a middle m between two
+// E4M3 values both round alike; there the sign of x - m * s (one fma) decides.  Exact ties are
+// common: 16-bit values and the scale of one of them make about one in a thousand.
+// Whether a value needs that is seen from its codes: bounds of the quotient, x * r * (1 +- 2^-21),
+// that round to one code leave nothing to decide (rounding is monotonic), which costs a packed
+// multiply and a conversion more instead of five integer operations a value.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -84,17 +86,31 @@ __device__ __forceinline__ uint32_t absmax8_bits(const float (&v)[8]) {
   return m;
 }
 
-// A group's scale and its reciprocal.  `exact`: the reciprocal is out of its safe range (a
-// subnormal, huge or non-finite scale), every quotient is formed in 64 bits.
+// A group's scale and its reciprocal.  `exact`: the scale is out of the safe range (subnormal,
+// huge or non-finite), every quotient is formed in 64 bits.
 struct F8Scale {
   float s, r;
   bool exact;
 };
+__device__ __forceinline__ float rcp_approx(float x) {   // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ F8Scale f8_scale(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
   F8Scale q;
-  q.s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
-  q.exact = !(q.s == 0.0f || (q.s > 0x1p-100f && q.s < 0x1p100f));
-  q.r = q.s == 0.0f ? 0.0f : __frcp_rn(q.s);
+  // a / 448: the product with the rounded 1/448 is within an ulp, and one residual step (exact
+  // in an fma) makes it the correctly rounded quotient
+  const float k = 1.0f / 448.0f;
+  const float q0 = __fmul_rn(a, k);
+  q.s = __fmaf_rn(__fmaf_rn(-q0, 448.0f, a), k, q0);
+  q.exact = !(amax_bits - 0x10000000u < 0x60000000u);   // a outside [2^-95, 2^97): 0 and NaN too
+  if (q.exact) {
+    q.s = __fdiv_rn(a, 448.0f);
+    q.exact = q.s != 0.0f;
+  }
+  q.r = q.s == 0.0f ? 0.0f : rcp_approx(q.s);
   return q;
 }
 
@@ -121,28 +137,57 @@ __device__ __forceinline__ uint32_t f8_pair(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// A value beside the quotient x / s that rounds to E4M3 as the quotient does, from a t that is
+// near a middle: the middle itself for a tie, else its fp32 neighbour on the quotient's side.
+__device__ __forceinline__ float f8_settle(float x, float s, float t) {
+  const uint32_t b = abs_bits(t);
+  uint32_t m = b >= 0x3C800000u ? (b & 0xFFF00000u) | 0x80000u : (b + 4u) & 0xFFF00000u;
+  const float e = __fmaf_rn(-__uint_as_float(m), s, fabsf(x));
+  m += e > 0.0f ? 1u : e < 0.0f ? 0xFFFFFFFFu : 0u;
+  return copysignf(__uint_as_float(m), t);
+}
+
+// One value's rounding input.
+__device__ __forceinline__ float f8_quotient(float x, const F8Scale& q) {
+  if (q.exact) return f8_quotient_exact(x, q.s);
+  const float t = __fmul_rn(x, q.r);
+  return f8_near_middle(t) ? f8_settle(x, q.s, t) : t;
+}
+
 // The E4M3 codes of 8 values of one group.
 __device__ __forceinline__ uint2 f8_codes8(const float (&v)[8], const F8Scale& q) {
-  float t[8];
-  bool near = q.exact;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t[i] = __fmul_rn(v[i], q.r);
-    near |= f8_near_middle(t[i]);
-  }
-  if (near) {
+  if (q.exact) {
+    uint2 c = make_uint2(0u, 0u);
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       float x = v[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) x = i == j ? v[j] : x;
-      const float f = f8_quotient_exact(x, q.s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = i == j ? f : t[j];
+      const uint32_t code = f8_pair(f8_quotient_exact(x, q.s), 0.0f) << (8 * (i & 3));
+      if (i < 4) c.x |= code; else c.y |= code;
     }
+    return c;
   }
-  return make_uint2(f8_pair(t[0], t[1]) | (f8_pair(t[2], t[3]) << 16),
-                    f8_pair(t[4], t[5]) | (f8_pair(t[6], t[7]) << 16));
+  const float rl = q.r * (1.0f - 0x1p-21f), rh = q.r * (1.0f + 0x1p-21f);
+  const float2 rl2 = make_float2(rl, rl), rh2 = make_float2(rh, rh);
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
+    const float2 l = __fmul2_rn(x, rl2), h = __fmul2_rn(x, rh2);
+    lo[i] = f8_pair(l.x, l.y);
+    hi[i] = f8_pair(h.x, h.y);
+  }
+  uint2 c = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  const uint2 d = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+  if (c.x != d.x || c.y != d.y) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = f8_quotient(v[i], q);
+    c = make_uint2(f8_pair(t[0], t[1]) | (f8_pair(t[2], t[3]) << 16),
+                   f8_pair(t[4], t[5]) | (f8_pair(t[6], t[7]) << 16));
+  }
+  return c;
 }
 
 // Maximum over the 16 lanes of this half-warp.

@@ -569,9 +569,11 @@ apex_status_t apex_block_norm(const void* x, int32_t dtype, int64_t T, int64_t H
   };
   auto by_width = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    if (H <= 8192) return run(apex::block_norm_kernel<DT, 1>, 1);
-    if (H <= 16384) return run(apex::block_norm_kernel<DT, 2>, 2);
-    return run(apex::block_norm_kernel<DT, 4>, 4);
+    const bool many = T >= 2 * (int64_t)dev_info().sms;
+    if (many && H <= 8192) return run(apex::block_norm_kernel<DT, 4, 256, 3>, 4);
+    if (H <= 8192) return run(apex::block_norm_kernel<DT, 1, 1024, 1>, 1);
+    if (H <= 16384) return run(apex::block_norm_kernel<DT, 2, 1024, 1>, 2);
+    return run(apex::block_norm_kernel<DT, 4, 1024, 1>, 4);
   };
   return dtype == APEX_DTYPE_F16 ? by_width(std::integral_constant<int, apex::DT_F16>{})
                                  : by_width(std::integral_constant<int, apex::DT_BF16>{});

@@ -428,8 +428,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
               const F8Scale q = f8_scale(max(max(s_max[e], s_max[BT + e]),
                                              max(s_max[2 * BT + e], s_max[3 * BT + e])));
               const float h = (e & 1) ? acc[0][e / 2].y : acc[0][e / 2].x;
-              float v = __fmul_rn(h, q.r);
-              if (q.exact || f8_near_middle(v)) v = f8_quotient_exact(h, q.s);
+              const float v = f8_quotient(h, q);
               const size_t slot = (size_t)(x.row0 + tb + e);
               if (n < args.N) args.hq[slot * args.N + n] = (uint8_t)f8_pair(v, 0.0f);
               if (row == 0) args.hs[slot * args.NB + x.tn] = q.s;
