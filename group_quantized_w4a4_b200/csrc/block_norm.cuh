@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const NormArgs a
     if (a.codes) {   // 16 lanes hold one group (the shuffles are warp-wide)
       const F8Scale q = f8_scale(half_warp_max(absmax8_bits(z[i])));
       if (in) {
-        *reinterpret_cast<uint2*>(a.codes + base + c) = f8_codes8(z[i], q);
+        *reinterpret_cast<uint2*>(a.codes + base + c) = f8_codes8<true>(z[i], q);
         if ((threadIdx.x & 15) == 0) a.scales[(size_t)blockIdx.x * a.G + c / 128] = q.s;
       }
     }
@@ -158,14 +158,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
     const long long t = i / chunks;
     const int c = (int)(i - t * chunks) * 8;
     float acc[8] = {};
-    for (int j = 0; j < k; ++j) {
-      const int id = __ldg(ids + t * k + j);
-      if (id < 0 || id >= E) continue;
-      const float w = __ldg(weights + t * k + j);
-      float v[8];
-      load8<DT>(y, (size_t)(t * k + j) * H + c, v);
+    for (int j0 = 0; j0 < k; j0 += 4) {   // four rows in flight
+      uint4 r[4];
+      float w[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+      for (int u = 0; u < 4; ++u) {
+        const int id = j0 + u < k ? __ldg(ids + t * k + j0 + u) : -1;
+        w[u] = 0.0f;
+        r[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (id >= 0 && id < E) {
+          w[u] = __ldg(weights + t * k + j0 + u);
+          r[u] = raw8(y, (size_t)(t * k + j0 + u) * H + c);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float v[8];
+        widen8<DT>(r[u], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[u], v[e], acc[e]);
+      }
     }
     *reinterpret_cast<uint4*>(static_cast<typename D::T*>(out) + (size_t)t * H + c) =
         make_uint4(D::pack(acc[0], acc[1]), D::pack(acc[2], acc[3]), D::pack(acc[4], acc[5]),

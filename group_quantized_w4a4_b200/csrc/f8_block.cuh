@@ -154,20 +154,38 @@ __device__ __forceinline__ float f8_quotient(float x, const F8Scale& q) {
   return f8_near_middle(t) ? f8_settle(x, q.s, t) : t;
 }
 
-// The E4M3 codes of 8 values of one group.
-__device__ __forceinline__ uint2 f8_codes8(const float (&v)[8], const F8Scale& q) {
-  if (q.exact) {
-    uint2 c = make_uint2(0u, 0u);
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      float x = v[0];
+// The E4M3 codes of 8 values of one group, where some value is near a middle or the scale is out
+// of its safe range.
+__device__ __forceinline__ uint2 f8_codes8_near(const float (&v)[8], const F8Scale& q) {
+  float t[8];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) x = i == j ? v[j] : x;
-      const uint32_t code = f8_pair(f8_quotient_exact(x, q.s), 0.0f) << (8 * (i & 3));
-      if (i < 4) c.x |= code; else c.y |= code;
-    }
-    return c;
+  for (int i = 0; i < 8; ++i) {
+    t[i] = __fmul_rn(v[i], q.r);
+    if (f8_near_middle(t[i])) t[i] = f8_settle(v[i], q.s, t[i]);
   }
+  return make_uint2(f8_pair(t[0], t[1]) | (f8_pair(t[2], t[3]) << 16),
+                    f8_pair(t[4], t[5]) | (f8_pair(t[6], t[7]) << 16));
+}
+__device__ __noinline__ uint2 f8_codes8_rare(float v0, float v1, float v2, float v3, float v4,
+                                             float v5, float v6, float v7, float s, float r,
+                                             bool exact) {
+  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+  F8Scale q;
+  q.s = s;
+  q.r = r;
+  q.exact = exact;
+  if (!exact) return f8_codes8_near(v, q);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = f8_quotient_exact(v[i], s);
+  return make_uint2(f8_pair(t[0], t[1]) | (f8_pair(t[2], t[3]) << 16),
+                    f8_pair(t[4], t[5]) | (f8_pair(t[6], t[7]) << 16));
+}
+
+// The E4M3 codes of 8 values of one group.  RARE: the values are fp32 results, which are near a
+// middle once in 10^5, so that case is a call; 16-bit values are so in one warp of five.
+template <bool RARE>
+__device__ __forceinline__ uint2 f8_codes8(const float (&v)[8], const F8Scale& q) {
   const float rl = q.r * (1.0f - 0x1p-21f), rh = q.r * (1.0f + 0x1p-21f);
   const float2 rl2 = make_float2(rl, rl), rh2 = make_float2(rh, rh);
   uint32_t lo[4], hi[4];
@@ -180,12 +198,13 @@ __device__ __forceinline__ uint2 f8_codes8(const float (&v)[8], const F8Scale& q
   }
   uint2 c = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
   const uint2 d = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-  if (c.x != d.x || c.y != d.y) {
-    float t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = f8_quotient(v[i], q);
-    c = make_uint2(f8_pair(t[0], t[1]) | (f8_pair(t[2], t[3]) << 16),
-                   f8_pair(t[4], t[5]) | (f8_pair(t[6], t[7]) << 16));
+  if constexpr (RARE) {
+    if (q.exact || c.x != d.x || c.y != d.y)
+      c = f8_codes8_rare(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], q.s, q.r, q.exact);
+  } else {
+    if (c.x != d.x || c.y != d.y) c = f8_codes8_near(v, q);
+    if (q.exact)
+      c = f8_codes8_rare(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], q.s, q.r, true);
   }
   return c;
 }
@@ -234,7 +253,7 @@ __global__ void __launch_bounds__(128) f8_quantize_act_kernel(const void* __rest
       const F8Scale q = f8_scale(half_warp_max(absmax8_bits(v[i])));
       if (in[i]) {
         *reinterpret_cast<uint2*>(codes + (size_t)row[i] * K + g[i] * 128 + hl * 8) =
-            f8_codes8(v[i], q);
+            f8_codes8<DT == DT_F32>(v[i], q);
       }
       if (hl == 0 && row[i] >= 0) scales[(size_t)row[i] * G + g[i]] = q.s;
     }
@@ -277,7 +296,7 @@ __global__ void __launch_bounds__(256) f8_pack_weights_kernel(const void* __rest
   for (int i = 0; i < 8; ++i) {
     const int n = nb * 128 + r0 + 16 * i;
     if (n < N && k < K)
-      *reinterpret_cast<uint2*>(codes + ((size_t)e * N + n) * K + k) = f8_codes8(v[i], q);
+      *reinterpret_cast<uint2*>(codes + ((size_t)e * N + n) * K + k) = f8_codes8<DT == DT_F32>(v[i], q);
   }
   if (threadIdx.x == 0) scales[((size_t)e * NB + nb) * G + g] = q.s;
 }

@@ -26,7 +26,7 @@
 // that stream (10.7 TB/s at 4096 x 8192 x 8192) is what bounded it; a pair needs 32 KB a CTA.
 // Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA (of the even CTA),
 // warps 2, 3 scales (global memory to a ring in shared memory, four K-groups of the 128 tokens
-// and of the tile's two weight blocks at a time), warps 4..11 epilogue (warp w: lanes
+// and of the tile's two weight blocks at a time, and which tile they are of), warps 4..11 epilogue (warp w: lanes
 // 32*(w%4).., half (w-4)/4 of the columns).  With its 128 accumulators and 64 partials in
 // flight an epilogue thread has no registers for scales on their way from memory: loaded
 // there, every fourth group waited 1,100 cycles for them.
@@ -84,7 +84,10 @@ struct FBCfg {
   static constexpr int OFF_SC = OFF_ST + EPI_WARPS * 4096;
   static constexpr int OFF_CUM = OFF_SC + SR * SC_BLOCK;           // [kMaxExperts + 1] ints
   static constexpr int OFF_AMAX = OFF_CUM + (kMaxExperts + 4) * 4;  // [2][2][128] words
-  static constexpr int OFF_BAR = OFF_AMAX + 2 * 2 * 128 * 4;
+  static constexpr int TR = 8;                     // ring of tile descriptions, 16 bytes each
+  static constexpr int OFF_TILE = OFF_AMAX + 2 * 2 * 128 * 4;
+  static constexpr int OFF_BAR = OFF_TILE + TR * 16;
+  static_assert(TR > SR, "a tile has at least one scale block");
   static constexpr int NBAR = 2 * NS + 2 * SLOTS + 1 + 2 * SR;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -168,7 +171,7 @@ __device__ __forceinline__ float at4(const float4& v, int j) {
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
+  return g * rcp_approx(1.0f + __expf(-g)) * u;
 }
 
 // Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k.
@@ -217,6 +220,7 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   int* s_cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
+  int4* s_tile = reinterpret_cast<int4*>(smem + C::OFF_TILE);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;                 // stage loaded (TMA bytes)
   uint64_t* empty = full + C::NS;        // stage read by its MMAs (commit)
@@ -389,9 +393,9 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
       if constexpr (!EXPERTS) grid_dep_wait();
       const int i0 = threadIdx.x - 64;          // rows i0 and i0 + 64 of this CTA's 128
       const bool s_vec = args.s_vec != 0;
-      int sb = 0;
+      int sb = 0, tno = 0;
       bool ok = true;
-      for (int t = t_first; ok && t < T; t += t_step) {
+      for (int t = t_first; ok && t < T; t += t_step, ++tno) {
         const ExpertTile x = tile_of(t);
         const float* sa[2];
 #pragma unroll
@@ -420,6 +424,8 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
           blk[i0] = v[0];
           blk[i0 + 64] = v[1];
           if (i0 < 2) blk[128 + i0] = w;
+          // (the scale blocks are at most SR ahead of the epilogue, so the tile's place is free)
+          if (i0 == 0 && gb == 0) s_tile[tno % C::TR] = make_int4(x.e, x.row0, x.rows, x.tn);
           mbar_arrive(smem_u32(&sfull[b]));
         }
       }
@@ -442,18 +448,17 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     };
     float2 acc[C::CPT / 2];
     bool ok = true;
-    int it = 0, sb = 0;
-    uint32_t par = 0;
-    for (int t = t_first; ok && t < T; t += t_step, par ^= 1u) {
-      const ExpertTile x = tile_of(t);
-      const bool live = trow < x.rows;
-      const int s = x.row0 + (live ? trow : 0);
+    int it = 0, sb = 0, tno = 0;
+    for (int t = t_first; ok && t < T; t += t_step, ++tno) {
+      // the tile's first scale block comes with its description
+      ok = mbar_wait_warp(smem_u32(&sfull[sb % C::SR]), (uint32_t)(sb / C::SR) & 1u, lim, abort_flag);
+      const int4 xd = ok ? s_tile[tno % C::TR] : make_int4(0, 0, 0, 0);
+      const int x_row0 = xd.y, x_rows = xd.z, x_tn = xd.w;
+      const bool live = trow < x_rows;
+      const int s = x_row0 + (live ? trow : 0);
       int out_row = live ? s : -1;
-      if constexpr (KIND == FB_DOWN) {
-        if (live) {
-          out_row = __ldg(args.order + s);
-          if (out_row >= args.slots) out_row = -1;
-        }
+      if constexpr (KIND == FB_DOWN) {   // (checked where it is used, when it has arrived)
+        if (live) out_row = __ldg(args.order + s);
       }
 #pragma unroll
       for (int e = 0; e < C::CPT / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
@@ -485,7 +490,6 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
         tc_fence_after();
         return r;
       };
-      ok = mbar_wait_warp(block_bar(), block_par(), lim, abort_flag);
       if (ok) load_block();
       for (int g = 0; ok && g < G; ++g) {
         const int sl = it % C::SLOTS;
@@ -539,10 +543,10 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
           h[2 * e] = silu_mul(acc[e].x, acc[32 + e].x);
           h[2 * e + 1] = silu_mul(acc[e].y, acc[32 + e].y);
         }
-        const int n0 = x.tn * 128 + 64 * half;
+        const int n0 = x_tn * 128 + 64 * half;
 #pragma unroll
         for (int e = 0; e < 64; ++e) mx = max(mx, abs_bits(h[e]));   // columns past N are 0
-        uint32_t* am = s_amax + par * 256;
+        uint32_t* am = s_amax + (tno & 1) * 256;
         am[half * 128 + row] = mx;
         ok = !bar_red_or(1, 256, !ok);   // one decision for all epilogue warps
         if (ok) {
@@ -556,11 +560,11 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
               v0[i] = h[e + i];
               v1[i] = h[e + 8 + i];
             }
-            const uint2 a = f8_codes8(v0, q), b = f8_codes8(v1, q);
+            const uint2 a = f8_codes8<true>(v0, q), b = f8_codes8<true>(v1, q);
             *reinterpret_cast<uint4*>(stage + lane * 64 + (((e >> 4) ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(a.x, a.y, b.x, b.y);
           }
-          if (half == 0 && live) args.hs[(size_t)s * args.NB + x.tn] = q.s;
+          if (half == 0 && live) args.hs[(size_t)s * args.NB + x_tn] = q.s;
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -573,6 +577,7 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
           __syncwarp();
         }
       } else if (ok) {
+        if (KIND == FB_DOWN && out_row >= args.slots) out_row = -1;
 #pragma unroll
         for (int pass = 0; pass < C::CPT / 64; ++pass) {
 #pragma unroll
@@ -583,23 +588,38 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
                            D::pack(a[2].x, a[2].y), D::pack(a[3].x, a[3].y));
           }
           __syncwarp();
-          const int n = x.tn * BN + half * C::CPT + pass * 64 + (lane & 7) * 8;
+          const int n = x_tn * BN + half * C::CPT + pass * 64 + (lane & 7) * 8;
+          uint4 v[8];
+          int to[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
-            const int to = __shfl_sync(0xffffffffu, out_row, r);
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-            if (to < 0) continue;
-            typename D::T* dst = static_cast<typename D::T*>(args.y) + (size_t)to * args.N + n;
-            if (args.y_vec) {   // N % 8 == 0
-              if (n < args.N) *reinterpret_cast<uint4*>(dst) = v;
-            } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            to[i] = __shfl_sync(0xffffffffu, out_row, r);
+            v[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          }
+          if (args.y_vec) {   // N % 8 == 0
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n < args.N && to[i] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<typename D::T*>(args.y) +
+                                          (size_t)to[i] * args.N + n) = v[i];
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              int row_to = to[0];
+              uint4 w4 = v[0];
+#pragma unroll
+              for (int u = 1; u < 8; ++u)
+                if (u == i) {
+                  row_to = to[u];
+                  w4 = v[u];
+                }
+              if (row_to < 0) continue;
+              uint16_t* dst = static_cast<uint16_t*>(args.y) + (size_t)row_to * args.N + n;
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (n + e < args.N)
-                  reinterpret_cast<uint16_t*>(dst)[e] =
-                      (uint16_t)((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+                if (n + e < args.N) dst[e] = (uint16_t)((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
             }
           }
           __syncwarp();
