@@ -246,8 +246,9 @@ apex_status_t check_moe(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
 // four tokens a warp at most).
 constexpr int64_t kRoutePlanTokens = 64;
 constexpr int kRoutePlanWarps = 16;
+constexpr int64_t kRouteBatchTokens = 8192;
 // From this many choices on a cluster of 8 CTAs groups them.
-constexpr int64_t kPlanClusterChoices = 4096;
+constexpr int64_t kPlanClusterChoices = 16384;
 
 apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, int64_t T,
                          int32_t E, int32_t k, int32_t score, const void* bias_f32,
@@ -293,12 +294,15 @@ apex_status_t route_launch_t(const apex::RouteArgs& a, int32_t* offsets, int32_t
     return launched(launch_pdl(kern, 1u, 32u * warps, (size_t)(route > plan ? route : plan), s, a,
                                offsets, order));
   }
-  int64_t blocks = ceil_div(a.T, apex::kRouteWarps);
+  // many tokens: four neighbours a warp, whose weights (64-bit exponentials and quotients) are
+  // then computed together
+  const int batch = a.k <= 8 && a.T >= kRouteBatchTokens ? 4 : 1;
+  int64_t blocks = ceil_div(a.T, apex::kRouteWarps * batch);
   const int64_t cap = (int64_t)dev_info().sms * 16;
   if (blocks > cap) blocks = cap;
   return launched(launch_pdl(apex::route_kernel<DT, EPL>, (unsigned)blocks,
                              32 * apex::kRouteWarps,
-                             a.G > 1 ? (size_t)apex::kRouteWarps * a.E * 8 : 0, s, a));
+                             a.G > 1 ? (size_t)apex::kRouteWarps * a.E * 8 : 0, s, a, batch));
 }
 
 template <int DT>

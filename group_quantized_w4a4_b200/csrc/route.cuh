@@ -7,16 +7,22 @@
 //   v; experts of the topk_groups best groups stay in the choice
 //   ids = the k largest v, ties to the lowest index;  weights = scale * p[ids], divided by
 //   their sum first when renormalized.
-// The choice is that of v in 64 bits; without a bias and groups the order of v is the order of
-// z, which is compared itself.  A NaN is chosen last; a softmax row of -inf alone has scores 0;
-// weights whose sum is 0 stay 0.
+// The choice is that of v in 64 bits; without a bias the order of v is the order of z, which is
+// compared itself.  A NaN is chosen last; a softmax row of -inf alone has scores 0; weights
+// whose sum is 0 stay 0.
 //
 // 64-bit exponentials of every logit cost 230 us for 16384 tokens x 256 experts, sixty times
-// the time of reading them.  So v is formed in fp32 with a bound f on its error, and the choice
-// is made on these; where two values that an order was decided between lie within their bounds
-// of each other (and do not come from the same logit and bias), the token is decided again in
-// 64 bits, which well under 1 % of random rows need.  Scores of the chosen experts are always
-// 64-bit.
+// the time of reading them.  So the choice is made on fp32 values with a bound on their errors
+// for the row.  Where two neighbours in the chosen order (or the last chosen and the best left)
+// are closer than their bounds, the chosen and the next few are compared again in 64 bits, a lane
+// each; where groups on either side of the border are, the whole token is.  The chosen experts'
+// scores are always 64-bit.
+//
+// The largest values are taken in turn.  Every lane first sorts its values as 32-bit keys whose
+// low bits are replaced by the register's number, so that a comparator is a maximum and a
+// minimum; a round is then one warp-wide maximum and a shift in the lane that had it.  (Values
+// that come from 16-bit logits as they are have those bits free: their keys hold the expert's
+// number and decide exactly, ties to the lowest index.)
 #pragma once
 #include <stdint.h>
 
@@ -55,15 +61,13 @@ __device__ __forceinline__ void merge2(F& best, F& second, F b2, F s2) {
   best = best >= b2 ? best : b2;
 }
 
-// Worth of the group of lanes 32/P.. (P = groups rounded up to a power of two) from the values
-// sv[E] in shared memory: every lane returns its group's (lanes of groups past G: -inf), and
-// the largest error bound sf[] of its members.
+// Worth of this lane's group, lane / lanes_per, from the values sv[E] in shared memory (lanes of
+// groups past G: -inf).
 template <typename F>
-__device__ __forceinline__ F group_worth(const F* sv, const float* sf, int E, int G, int lane,
-                                         int lanes_per, F ninf, float* fmax_out) {
+__device__ __forceinline__ F group_worth(const F* sv, int E, int G, int lane, int lanes_per,
+                                         F ninf) {
   const int epg = E / G, g = lane / lanes_per, s = lane % lanes_per;
   F best = ninf, second = ninf;
-  float f = 0.0f;
   if (g < G) {
     const int n = (epg + lanes_per - 1) / lanes_per;
     // groups start at different places of their round, so that they meet different banks
@@ -72,9 +76,8 @@ __device__ __forceinline__ F group_worth(const F* sv, const float* sf, int E, in
       const int at = s + lanes_per * i;
       if (at < epg) {
         const F w = sv[g * epg + at];
-        if (w > best) { second = best; best = w; }
-        else if (w > second) second = w;
-        if (sf) f = fmaxf(f, sf[g * epg + at]);
+        second = w > best ? best : w > second ? w : second;
+        best = w > best ? w : best;
       }
       i = i + 1 == n ? 0 : i + 1;
     }
@@ -82,10 +85,8 @@ __device__ __forceinline__ F group_worth(const F* sv, const float* sf, int E, in
   for (int o = 1; o < lanes_per; o <<= 1) {
     const F b2 = __shfl_xor_sync(0xffffffffu, best, o);
     const F s2 = __shfl_xor_sync(0xffffffffu, second, o);
-    f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o));
     merge2(best, second, b2, s2);
   }
-  if (fmax_out) *fmax_out = f;
   return epg > 1 ? best + second : best;
 }
 
@@ -108,51 +109,64 @@ __device__ __forceinline__ int lanes_per_group(int G) {
   return p;
 }
 
+// A logit's score before normalization, in 64 bits.
+__device__ __forceinline__ double route_score64(float z, bool sigmoid, float m) {
+  if (sigmoid) return 1.0 / (1.0 + exp(-(double)z));
+  return m == ninf_f() && z == m ? 0.0 : exp((double)z - (double)m);
+}
+
+// The sum of a softmax row's scores in 64 bits.
+template <int DT>
+__device__ __forceinline__ double route_sum64(const typename DTraits<DT>::T* z, int E, float m,
+                                              int lane) {
+  double sum = 0.0;
+#pragma unroll 2
+  for (int e = lane; e < E; e += 32) sum += route_score64(DTraits<DT>::up(z[e]), false, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
 // The whole choice in 64 bits; returns lane j's j-th expert.
 template <int DT, int EPL>
 __device__ __noinline__ int route_exact(const typename DTraits<DT>::T* z, const RouteArgs& a,
                                         float m, double* sv, int lane) {
   const int E = a.E;
+  const double sum = a.sigmoid ? 1.0 : route_sum64<DT>(z, E, m, lane);
   double v[EPL];
-  double sum = 0.0;
+  uint32_t left = 0;
 #pragma unroll 1
   for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
     double w = ninf_d();
-    if (lane + 32 * i < E) {
-      const float zi = DTraits<DT>::up(z[lane + 32 * i]);
-      if (a.sigmoid) w = 1.0 / (1.0 + exp(-(double)zi));
-      else w = m == ninf_f() && zi == m ? 0.0 : exp((double)zi - (double)m);
-      sum += w;
+    if (e < E) {
+      left |= 1u << i;
+      w = route_score64(DTraits<DT>::up(z[e]), a.sigmoid, m);
+      if (!a.sigmoid) w = sum == 0.0 ? 0.0 : w / sum;
+      if (a.bias) w += (double)a.bias[e];
+      if (!(w == w)) w = ninf_d();
+      if (a.G > 1) sv[e] = w;
     }
 #pragma unroll
     for (int c = 0; c < EPL; ++c) v[c] = c == i ? w : v[c];
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  uint32_t left = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) {
-      left |= 1u << i;
-      if (!a.sigmoid) v[i] = sum == 0.0 ? 0.0 : v[i] / sum;
-      if (a.bias) v[i] += (double)a.bias[e];
-      if (!(v[i] == v[i])) v[i] = ninf_d();
-    }
-  }
   if (a.G > 1) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E) sv[lane + 32 * i] = v[i];
     __syncwarp();
     const int lp = lanes_per_group(a.G);
-    const double worth = group_worth<double>(sv, nullptr, E, a.G, lane, lp, ninf_d(), nullptr);
+    const double worth = group_worth<double>(sv, E, a.G, lane, lp, ninf_d());
     __syncwarp();
     const uint32_t open = open_groups(worth, a.G, a.TG, lane, lp);
     const int epg = E / a.G;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (lane + 32 * i < E && !((open >> ((lane + 32 * i) / epg)) & 1u)) left &= ~(1u << i);
+  }
+  if (!a.bias) {   // the order of the logits
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const double w = lane + 32 * i < E ? (double)DTraits<DT>::up(z[lane + 32 * i]) : ninf_d();
+      v[i] = w == w ? w : ninf_d();
+    }
   }
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
@@ -178,197 +192,318 @@ __device__ __noinline__ int route_exact(const typename DTraits<DT>::T* z, const 
   return mine;
 }
 
+// Lane c < n holds candidate expert `id`, all of a token's choice among them: their order by the
+// exact values; returns lane j's j-th.
+template <int DT>
+__device__ __noinline__ int route_candidates(const typename DTraits<DT>::T* z, const RouteArgs& a,
+                                             float m, int id, int n, int lane) {
+  const double sum = a.bias && !a.sigmoid ? route_sum64<DT>(z, a.E, m, lane) : 1.0;
+  double v = ninf_d();
+  if (lane < n) {
+    const float zi = DTraits<DT>::up(z[id]);
+    v = !a.bias ? (double)zi : route_score64(zi, a.sigmoid, m);
+    if (a.bias) v = (a.sigmoid ? v : sum == 0.0 ? 0.0 : v / sum) + (double)a.bias[id];
+    if (!(v == v)) v = ninf_d();
+  }
+  int rank = 0;
+  for (int c = 0; c < n; ++c) {
+    const double o = __shfl_sync(0xffffffffu, v, c);
+    const int oid = __shfl_sync(0xffffffffu, id, c);
+    rank += o > v || (o == v && oid < id);
+  }
+  int mine = -1;
+  for (int c = 0; c < n; ++c) {
+    const int r = __shfl_sync(0xffffffffu, rank, c);
+    const int oid = __shfl_sync(0xffffffffu, id, c);
+    if (r == lane) mine = oid;
+  }
+  return mine;
+}
+
+// What the last step needs of a token whose experts are chosen.
+struct RouteChoice {
+  int id;         // lane j: the j-th expert (-1: the token is masked)
+  float m;        // softmax: the row's largest logit
+  double sum;     // softmax without renormalization: the sum of exp(z - m)
+  bool poison;    // softmax: a NaN or +inf logit makes every score NaN
+};
+
+// Sorts EPL keys in descending order (odd-even merge sort network; EPL a power of two).
+template <int EPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[EPL]) {
+#pragma unroll
+  for (int p = 1; p < EPL; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < EPL; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < EPL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = k[i + j], y = k[i + j + q];
+            k[i + j] = max(x, y);
+            k[i + j + q] = min(x, y);
+          }
+}
+
 // One token by one warp; lane l holds experts l, l + 32, ...  sv: E doubles of this warp's
 // shared memory (used with groups only).
 template <int DT, int EPL>
-__device__ __forceinline__ void route_token(const RouteArgs& a, long long t, double* sv, int lane) {
-  if (a.mask && !a.mask[t]) {
-    if (lane < a.k) {
-      a.ids[t * a.k + lane] = -1;
-      a.weights[t * a.k + lane] = 0.0f;
-    }
-    return;
-  }
+__device__ __forceinline__ void route_load(const RouteArgs& a, long long t, int lane,
+                                           float (&zv)[EPL]) {
+  const typename DTraits<DT>::T* z =
+      static_cast<const typename DTraits<DT>::T*>(a.logits) + t * a.E;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    zv[i] = lane + 32 * i < a.E ? DTraits<DT>::up(z[lane + 32 * i]) : ninf_f();
+}
+
+template <int DT, int EPL>
+__device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long long t,
+                                                    const float (&zv)[EPL], double* sv,
+                                                    float bmax, int lane) {
+  RouteChoice r;
+  r.id = -1;
+  r.m = ninf_f();
+  r.sum = 0.0;
+  r.poison = false;
+  if (a.mask && !a.mask[t]) return r;
   const int E = a.E;
   const typename DTraits<DT>::T* z = static_cast<const typename DTraits<DT>::T*>(a.logits) + t * E;
   const bool plain = a.bias == nullptr && a.G == 1;
-  float zf[EPL];
+  float v[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    zf[i] = lane + 32 * i < E ? DTraits<DT>::up(z[lane + 32 * i]) : ninf_f();
-  float m = ninf_f();
-  bool poison = false;    // softmax: a NaN or +inf logit makes every score NaN
-  double sum = 0.0;       // softmax: of exp(z - m) over the row
-  float v[EPL], f[EPL];   // fp32 values that are compared, and bounds on their errors
+  for (int i = 0; i < EPL; ++i) v[i] = zv[i];
+  float F = 0.0f;   // bound on the error of every v
   if (!a.sigmoid) {
     bool nan = false;
-    uint32_t mk = 0;
+    float m = ninf_f();
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      nan |= !(zf[i] == zf[i]);
-      mk = max(mk, zf[i] == zf[i] ? route_key(zf[i]) : 0u);
+      nan |= !(v[i] == v[i]);
+      m = fmaxf(m, v[i]);
     }
-    mk = __reduce_max_sync(0xffffffffu, mk);
-    m = mk == 0u ? ninf_f() : __uint_as_float((mk & 0x80000000u) ? mk & 0x7FFFFFFFu : ~mk);
-    poison = __any_sync(0xffffffffu, nan) || m == -ninf_f();
-    if (!(plain && a.renorm)) {
-      // exp(z - m) with the rounding of z - m made good: within 1.5 ulp of the exact value
+    const uint32_t mk = __reduce_max_sync(0xffffffffu, route_key(m));
+    m = __uint_as_float((mk & 0x80000000u) ? mk & 0x7FFFFFFFu : ~mk);
+    r.m = m;
+    r.poison = __any_sync(0xffffffffu, nan) || m == -ninf_f();
+    if (!plain || !a.renorm) {
+      float sum = 0.0f;
+      float e[EPL];
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const float d = zf[i] - m;
-        const float lost = fabsf(zf[i]) > fabsf(m) ? -m - (d - zf[i]) : zf[i] - (d + m);
-        const float e = zf[i] == ninf_f() ? 0.0f : expf(d);
-        v[i] = fabsf(lost) < 1.0f ? fmaf(e, lost, e) : e;
-        if (lane + 32 * i >= E) v[i] = 0.0f;
-        sum += (double)v[i];
+        // exp(z - m) with the rounding of z - m made good: within 1.5 ulp of the exact value
+        const float d = v[i] - m;
+        const float lost = fabsf(v[i]) > fabsf(m) ? -m - (d - v[i]) : v[i] - (d + m);
+        e[i] = v[i] == ninf_f() ? 0.0f : a.renorm ? __expf(d) : expf(d);
+        e[i] = fabsf(lost) < 1.0f ? fmaf(e[i], lost, e[i]) : e[i];
+        sum += e[i];
+        r.sum += (double)e[i];
+      }
+      if (!a.renorm) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-  }
-  if (plain) {
+      if (!plain) {
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        // The sum: EPL + 5 roundings (under 2^-19.5 together) and its terms' errors, the fast
+        // exponential's (2 + 1.2 |d|) 2^-23 with |d| = 7 at most on average.  A score's own:
+        // 2^-22 of it, and 1.2 |d| p 2^-23 <= 0.5 top 2^-23.
+        F = inv * 0x1p-18f + 0x1p-23f;   // inv: the largest score
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = zf[i];
-  } else {
-    const float inv = sum == 0.0 ? 0.0f : __double2float_rn(1.0 / sum);
-    // relative error bounds: softmax 1.5 ulp of the exponential, as much of the sum, 1/sum and
-    // the product (one rounding each): under 2^-20; sigmoid: 1 ulp of the exponential and the
-    // roundings of the sum and the quotient: under 2^-21
-    const float rel = a.sigmoid ? 0x1p-21f : 0x1p-20f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float p = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-zf[i])) : v[i] * inv;
-      v[i] = p;
-      if (a.bias && lane + 32 * i < E) v[i] = p + __ldg(a.bias + lane + 32 * i);
-      f[i] = p * rel + fabsf(v[i]) * 0x1p-23f + 0x1p-126f;
-      if (!(f[i] < 1e30f)) f[i] = 1e30f;   // NaN or huge: decide in 64 bits
-    }
-  }
-  uint32_t key[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    key[i] = lane + 32 * i >= E ? 0u : v[i] == v[i] ? route_key(v[i]) : route_key(ninf_f());
-  bool unsure = false;
-  if (a.G > 1) {
-    float* s32 = reinterpret_cast<float*>(sv);   // v, then f
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E) {
-        s32[lane + 32 * i] = v[i] == v[i] ? v[i] : ninf_f();
-        s32[E + lane + 32 * i] = f[i];
+        for (int i = 0; i < EPL; ++i) v[i] = e[i] * inv;
       }
-    __syncwarp();
-    const int lp = lanes_per_group(a.G);
-    float ferr;
-    const float worth = group_worth<float>(s32, s32 + E, E, a.G, lane, lp, ninf_f(), &ferr);
-    __syncwarp();
-    const uint32_t open = open_groups(worth, a.G, a.TG, lane, lp);
-    if (a.TG < a.G) {
-      // two values, each within ferr, and the rounding of their sum
-      const float err = 2.0f * ferr + fabsf(worth) * 0x1p-23f;
-      const int g = lane / lp;
-      const bool kept = g < a.G && ((open >> g) & 1u);
-      float low = kept ? worth - err : -ninf_f();
-      float high = g < a.G && !kept ? worth + err : ninf_f();
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-      }
-      unsure = !(low > high);
     }
-    const int epg = E / a.G;
+  } else if (!plain) {
+    // 1 / (1 + exp(-z)): the fast exponential's relative error (2 + 1.2 |z|) 2^-23 counts
+    // p (1 - p) times, p (1 - p) |z| < 0.23; with the sum's rounding and the reciprocal's ulp
+    // under 2^-22 in all
+    F = 0x1p-21f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E && !((open >> ((lane + 32 * i) / epg)) & 1u)) key[i] = 0u;
-  }
-  int mine = -1;             // lane j: the j-th choice
-  float mine_v = 0.0f, mine_f = 0.0f, mine_z = 0.0f, mine_b = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t bk = key[0];
-    int bi = 0;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i)
-      if (key[i] > bk) { bk = key[i]; bi = i; }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-    const uint32_t be =
-        __reduce_min_sync(0xffffffffu, bk == top ? (uint32_t)(lane + 32 * bi) : 0xFFFFFFFFu);
-    if (lane == j) mine = (int)be;
-    if ((be & 31u) == (uint32_t)lane) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if ((int)(be >> 5) == i) key[i] = 0u;
-    }
+    for (int i = 0; i < EPL; ++i) v[i] = rcp_approx(1.0f + __expf(-v[i]));
   }
   if (!plain) {
-    // every chosen value against the next, and the last against all that were left (the ones
-    // still with a key)
-    const int src = mine < 0 ? 0 : mine;
+    F += (1.0f + bmax) * 0x1p-23f;
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      // lane j's expert lives in lane (mine & 31), register mine >> 5
-      const float vv = __shfl_sync(0xffffffffu, v[i], src & 31);
-      const float ff = __shfl_sync(0xffffffffu, f[i], src & 31);
-      const float zz = __shfl_sync(0xffffffffu, zf[i], src & 31);
-      if ((src >> 5) == i) { mine_v = vv; mine_f = ff; mine_z = zz; }
+      for (int i = 0; i < EPL; ++i)
+        if (lane + 32 * i < E) v[i] += __ldg(a.bias + lane + 32 * i);
     }
-    mine_b = a.bias ? __ldg(a.bias + src) : 0.0f;
-    const float nv = __shfl_down_sync(0xffffffffu, mine_v, 1);
-    const float nf = __shfl_down_sync(0xffffffffu, mine_f, 1);
-    const float nz = __shfl_down_sync(0xffffffffu, mine_z, 1);
-    const float nb = __shfl_down_sync(0xffffffffu, mine_b, 1);
-    if (lane + 1 < a.k)
-      unsure |= !(mine_v - nv > mine_f + nf) && !(mine_z == nz && mine_b == nb);
-    const float lv = __shfl_sync(0xffffffffu, mine_v, a.k - 1);
-    const float lf = __shfl_sync(0xffffffffu, mine_f, a.k - 1);
-    const float lz = __shfl_sync(0xffffffffu, mine_z, a.k - 1);
-    const float lb = __shfl_sync(0xffffffffu, mine_b, a.k - 1);
+  }
+  uint32_t open = 0xffffffffu;
+  const int epg = E / a.G;
+  bool unsure = false;
+  if (a.G > 1) {
+    float* s32 = reinterpret_cast<float*>(sv);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (key[i] != 0u && !(lv - v[i] > lf + f[i]) &&
-          !(zf[i] == lz && (!a.bias || __ldg(a.bias + lane + 32 * i) == lb)))
-        unsure = true;
-    if (__any_sync(0xffffffffu, unsure)) mine = route_exact<DT, EPL>(z, a, m, sv, lane);
+      if (lane + 32 * i < E) s32[lane + 32 * i] = v[i] == v[i] ? v[i] : ninf_f();
+    __syncwarp();
+    const int lp = lanes_per_group(a.G);
+    const float worth = group_worth<float>(s32, E, a.G, lane, lp, ninf_f());
+    __syncwarp();
+    open = open_groups(worth, a.G, a.TG, lane, lp);
+    if (a.TG < a.G) {
+      // two values, each within F, and the rounding of their sum, on either side of the border
+      const float err = 2.0f * F + fabsf(worth) * 0x1p-23f;
+      const int g = lane / lp;
+      const bool kept = g < a.G && ((open >> g) & 1u);
+      // (as keys, for one warp-wide minimum and maximum; a NaN decides nothing: 64 bits)
+      const uint32_t low = kept ? route_key(worth - err) : 0xffffffffu;
+      const uint32_t high = g < a.G && !kept ? route_key(worth + err) : 0u;
+      unsure = __reduce_min_sync(0xffffffffu, low) <= __reduce_max_sync(0xffffffffu, high);
+    }
   }
-  // the chosen scores in 64 bits
+  // keys: the value (without a bias: the logit) in the upper bits, NaN as -inf and a closed or
+  // absent expert as 0; below it the register's number, or the whole expert's where 16-bit
+  // logits leave those bits free
+  constexpr bool HALF = DT != DT_F32;
+  const bool whole = HALF && a.bias == nullptr;
+  const uint32_t low_bits = whole ? 511u : (uint32_t)(EPL - 1);
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
+    const bool in = e < E && (a.G == 1 || ((open >> (e / epg)) & 1u));
+    const float w = a.bias ? v[i] : zv[i];
+    const uint32_t k32 = route_key(w == w ? w : ninf_f());
+    const uint32_t low = low_bits - (whole ? (uint32_t)e : (uint32_t)i);
+    key[i] = in ? (k32 & ~low_bits) | low : 0u;
+    unsure |= !whole && !(w == w);   // NaNs tie with -inf
+  }
+  sort_keys<EPL>(key);
+  uint32_t mine = 0;   // lane j: the j-th largest key
+  auto rounds = [&](int from, int to) {
+    for (int j = from; j < to; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+      const int winner = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
+      if (lane == j) {
+        mine = top;
+        r.id = whole ? (int)(511u - (top & 511u)) : winner + 32 * (int)(low_bits - (top & low_bits));
+      }
+      if (lane == winner) {
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+        key[EPL - 1] = 0u;
+      }
+    }
+  };
+  if (whole) {
+    rounds(0, a.k);
+    if (__any_sync(0xffffffffu, unsure)) r.id = route_exact<DT, EPL>(z, a, r.m, sv, lane);
+  } else {
+    rounds(0, min(32, a.k + 1));
+    if (a.bias == nullptr) F = 0.0f;   // logits are compared as they are
+    // neighbours in the order that are not clearly apart (key 0: nothing was left)
+    auto decode = [](uint32_t k) {
+      return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+    };
+    const float cut = (float)EPL * 0x1p-23f;   // what the keys' low bits hide, relative
+    auto apart = [&](uint32_t hi, uint32_t lo) {
+      const float x = decode(hi), y = decode(lo);
+      return lo == 0u || x - y > 2.0f * F + cut * (fabsf(x) + fabsf(y)) + 0x1p-120f;
+    };
+    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+    const bool close = lane < a.k && !(lane < 31 && apart(mine, next));
+    if (__any_sync(0xffffffffu, close || unsure)) {
+      const int n = min(32, a.k + 8);   // candidates: the choice is among them if the last is out
+      rounds(min(32, a.k + 1), n);
+      const uint32_t kth = __shfl_sync(0xffffffffu, mine, a.k - 1);
+      const uint32_t last = __shfl_sync(0xffffffffu, mine, n - 1);
+      if (!__any_sync(0xffffffffu, unsure) && n > a.k && apart(kth, last))
+        r.id = route_candidates<DT>(z, a, r.m, r.id,
+                                    __popc(__ballot_sync(0xffffffffu, lane < n && mine != 0u)), lane);
+      else
+        r.id = route_exact<DT, EPL>(z, a, r.m, sv, lane);
+    }
+  }
+  return r;
+}
+
+// The weights of up to 32 / kp tokens at once, kp lanes each: lane b * kp + j has the j-th choice
+// of token t0 + b.  Scores in 64 bits, one rounding.
+template <int DT>
+__device__ __forceinline__ void route_write(const RouteArgs& a, long long t0, int batch, int kp,
+                                            const RouteChoice& r, int lane) {
+  const int b = lane / kp, j = lane - b * kp;
+  const long long t = t0 + b;
+  const bool mine = b < batch && j < a.k && t < a.T;
   double p = 0.0;
-  if (lane < a.k) {
-    const float zm = DTraits<DT>::up(z[mine]);
+  if (mine && r.id >= 0) {
+    const float zm = DTraits<DT>::up(
+        static_cast<const typename DTraits<DT>::T*>(a.logits)[t * a.E + r.id]);
     if (a.sigmoid) p = 1.0 / (1.0 + exp(-(double)zm));
-    else p = m == ninf_f() && zm == m ? 0.0 : exp((double)zm - (double)m);
-    if (poison) p = __longlong_as_double(0x7FF8000000000000ll);
-    if (!a.sigmoid && !a.renorm && sum != 0.0) p /= sum;
+    else p = r.m == ninf_f() && zm == r.m ? 0.0 : exp((double)zm - (double)r.m);
+    if (r.poison) p = __longlong_as_double(0x7FF8000000000000ll);
+    if (!a.sigmoid && !a.renorm && r.sum != 0.0) p /= r.sum;
   }
   if (a.renorm) {
     double total = p;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = kp >> 1; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     p = total == 0.0 ? 0.0 : p / total;
   }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = mine;
-    a.weights[t * a.k + lane] = __double2float_rn(p * (double)a.scale);
+  if (mine) {
+    a.ids[t * a.k + j] = r.id;
+    a.weights[t * a.k + j] = __double2float_rn(p * (double)a.scale);
+  }
+}
+
+// Tokens first, first + step, ..., `batch` (32 / kp at most) neighbours at a time.
+template <int DT, int EPL>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first, long long step,
+                                             int batch, double* sv, int lane) {
+  float bmax = 0.0f;
+  if (a.bias)
+    for (int e = lane; e < a.E; e += 32) bmax = fmaxf(bmax, fabsf(__ldg(a.bias + e)));
+  bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+  int kp = 1;
+  while (kp < a.k) kp <<= 1;
+  for (long long t0 = first * batch; t0 < a.T; t0 += step * batch) {
+    RouteChoice all;
+    all.id = -1;
+    all.m = 0.0f;
+    all.sum = 0.0;
+    all.poison = false;
+    float zv[EPL];
+    route_load<DT, EPL>(a, t0, lane, zv);
+    for (int b = 0; b < batch && t0 + b < a.T; ++b) {
+      float zn[EPL];   // the next token's logits are on their way meanwhile
+      if (b + 1 < batch && t0 + b + 1 < a.T) route_load<DT, EPL>(a, t0 + b + 1, lane, zn);
+      const RouteChoice r = route_choose<DT, EPL>(a, t0 + b, zv, sv, bmax, lane);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) zv[i] = zn[i];
+      const int id = __shfl_sync(0xffffffffu, r.id, lane & (kp - 1));
+      if (lane / kp == b) {
+        all = r;
+        all.id = id;
+      }
+    }
+    route_write<DT>(a, t0, batch, kp, all, lane);
   }
 }
 
 template <int DT, int EPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a, int batch) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ double s_v[];   // [kRouteWarps][E] with groups
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < a.T;
-       t += (long long)gridDim.x * kRouteWarps)
-    route_token<DT, EPL>(a, t, s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
+  route_tokens<DT, EPL>(a, (long long)blockIdx.x * kRouteWarps + warp,
+                        (long long)gridDim.x * kRouteWarps, batch,
+                        s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
 }
 
 // Groups the flat indices i = t * k + j of ids by expert, in ascending order within each:
 // order, offsets; entries behind offsets[E] are -1.  An id outside [0, E) belongs to none.
 // A stable counting sort by one CTA, or by the CTAs of one cluster, which pass each other their
 // counts through shared memory.  Every warp owns a run of consecutive entries: it counts them
-// by expert (equal ids of 32 entries at once), the counts become the places of its first
-// entry of each expert, and a second walk writes.  No atomics: the result does not depend on
-// the order in which the warps run.
+// by expert, the counts become the places of its first entry of each expert, and a second walk
+// writes, with the places of equal ids among 32 from one ballot for each bit of an id (a
+// hardware match takes 60 cycles of a unit that the whole SM shares).  The atomics only count:
+// the result does not depend on the order in which the warps run.
+constexpr int kPlanBatch = 8;   // loads in flight
 struct PlanShared {
   int* cnt;     // [warps][E]
   int* tot;     // [E] of this CTA (read by the cluster's other CTAs)
@@ -387,12 +522,18 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
   int* mine = s.cnt + warp * E;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
   __syncwarp();
-  for (int i = begin + lane; i - lane < end; i += 32) {
-    const int id = i < end ? ids[i] : -1;
-    const bool in = id >= 0 && id < E;
-    const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
-    if (in && lane == __ffs(same) - 1) mine[id] += __popc(same);
-    __syncwarp();
+  int bits = 0;
+  while ((1 << bits) < E + 1) ++bits;
+  for (int i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
+    int id[kPlanBatch];
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      id[u] = i < end ? ids[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u)
+      if (id[u] >= 0 && id[u] < E) atomicAdd(mine + id[u], 1);   // counts alone: any order
   }
   __syncthreads();
   // counts -> exclusive sums over this CTA's warps, and the CTA's totals
@@ -449,17 +590,30 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
   if (rank == 0 && threadIdx.x == 0) offsets[E] = carry;
   for (int e = lane; e < E; e += 32) mine[e] += s.base[e];
   __syncwarp();
-  for (int i = begin + lane; i - lane < end; i += 32) {
-    const int id = i < end ? ids[i] : -1;
-    const bool in = id >= 0 && id < E;
-    const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
-    const int at = in ? mine[id] : 0;
-    __syncwarp();
-    if (in) {
-      order[at + __popc(same & ((1u << lane) - 1u))] = i;
-      if (lane == __ffs(same) - 1) mine[id] = at + __popc(same);
+  for (int i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
+    int id[kPlanBatch];
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      id[u] = i < end ? ids[i] : -1;
+      if (id[u] < 0 || id[u] >= E) id[u] = E;   // none
     }
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kPlanBatch; ++u) {
+      uint32_t same = 0xffffffffu;   // the lanes with this lane's id
+      for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(0xffffffffu, (id[u] >> b) & 1);
+        same &= ((id[u] >> b) & 1) ? set : ~set;
+      }
+      const bool in = id[u] < E;
+      const int at = in ? mine[id[u]] : 0;
+      __syncwarp();
+      if (in) {
+        order[at + __popc(same & ((1u << lane) - 1u))] = i0 + 32 * u + lane;
+        if (lane == __ffs(same) - 1) mine[id[u]] = at + __popc(same);
+      }
+      __syncwarp();
+    }
   }
   for (int i = carry + rank * (int)blockDim.x + (int)threadIdx.x; i < S; i += ctas * blockDim.x)
     order[i] = -1;
@@ -497,8 +651,7 @@ __global__ void __launch_bounds__(512) route_plan_kernel(const RouteArgs a, int3
   grid_dep_launch();
   extern __shared__ double s_v[];   // [warps][E] with groups; the counting sort's arrays after
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  for (int t = warp; t < a.T; t += warps)
-    route_token<DT, EPL>(a, t, s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
+  route_tokens<DT, EPL>(a, warp, warps, 1, s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
   __syncthreads();   // the ids in global memory are this CTA's own writes
   plan_experts_cta(a.ids, a.T * a.k, a.E, offsets, order,
                    plan_shared(reinterpret_cast<int*>(s_v), a.E, warps), 0, 1);

@@ -457,8 +457,8 @@ apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void 
  *     largest sum of their two largest v (one, where a group has one) stay in the choice
  *   ids [T][k] = the k largest v in descending order, ties to the lowest index
  *   weights [T][k] = scale * p[ids] (divided by their sum first with renormalize)
- * The choice is that of the exact scores: values are compared in 64 bits (the logits themselves
- * where there is neither a bias nor groups).  mask [T] bytes (NULL: all ones): a token with 0
+ * The choice is that of the exact scores: values are compared in 64 bits (without a bias the
+ * logits themselves, whose order is the same; a group's sum is that of its scores).  mask [T] bytes (NULL: all ones): a token with 0
  * gets ids -1 and weights 0.  NaN logits are chosen last and make weights NaN; a softmax row of
  * -inf alone has scores 0, and weights that sum to 0 stay 0.
  * E % groups == 0, k <= topk_groups * E / groups, E <= APEX_MAX_EXPERTS, k <= APEX_MAX_TOP_K,

@@ -104,11 +104,13 @@ def route(z, k, bias=None, score="softmax", groups=1, topk_groups=1, renormalize
                 p = 1 / (1 + np.exp(-row))
             elif np.all(row == -np.inf):
                 p = np.zeros(E)
+            elif np.all(np.isnan(row)):
+                p = row
             else:
                 p = np.exp(row - np.nanmax(row))
                 p = p / p.sum()
         scores[t] = p
-        v = row if bias is None and groups == 1 else p + (0 if bias is None else bias)
+        v = p + (0 if bias is None else bias)
         v = np.where(np.isnan(v), -np.inf, v)
         open_ = list(range(E))
         if groups > 1:
@@ -116,6 +118,8 @@ def route(z, k, bias=None, score="softmax", groups=1, topk_groups=1, renormalize
             worth = [sum(sorted(v[g * n:(g + 1) * n])[-2:]) for g in range(groups)]
             kept = sorted(range(groups), key=lambda g: (-worth[g], g))[:topk_groups]
             open_ = [e for e in open_ if e // n in kept]
+        if bias is None:      # the order of the scores is that of the logits
+            v = np.where(np.isnan(row), -np.inf, row)
         ids[t] = sorted(open_, key=lambda e: (-v[e], e))[:k]
         w = p[ids[t]]
         if renormalize:
