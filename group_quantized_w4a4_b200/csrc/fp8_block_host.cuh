@@ -51,23 +51,21 @@ cudaError_t set_smem(F kern, int bytes, int* attr_dev) {   // once per device an
   return e;
 }
 
-// Launches over `tiles` tiles (an upper bound for experts): one CTA, or pair of CTAs, per SM or
-// pair of SMs at most.
-template <int BN, int CG, int KIND, int DT>
+// Launches over `tiles` tiles (an upper bound for experts), one persistent CTA per SM at most.
+template <int BN, int KIND, int DT>
 apex_status_t launch_fb(const void* a_codes, int64_t a_rows, const void* w_codes, int64_t Z,
                         FBArgs a, int64_t tiles, cudaStream_t s) {
-  using C = FBCfg<BN, CG>;
-  auto kern = apex::f8_block_gemm_kernel<BN, CG, KIND, DT>;
+  using C = FBCfg<BN>;
+  auto kern = apex::f8_block_gemm_kernel<BN, KIND, DT>;
   static thread_local int attr_dev = -1;
   if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
   CUtensorMap ma, mb;
   if (!make_expanded_map(&ma, a_codes, a_rows, a.K, 128) ||
-      !make_codes3_map(&mb, w_codes, Z, a.N, a.K, C::BOX))
+      !make_codes3_map(&mb, w_codes, Z, a.N, a.K, 128))
     return APEX_ERR_CUDA;
-  const int64_t most = dev_info().sms / CG;
-  a.P = (int)(tiles < most ? tiles : most) * CG;
-  return launched(launch_pdl_cl(kern, (unsigned)a.P, (unsigned)C::THREADS, (size_t)C::SMEM, s,
-                                (unsigned)CG, ma, mb, a));
+  const int64_t most = dev_info().sms;
+  a.P = (int)(tiles < most ? tiles : most);
+  return launched(launch_pdl(kern, (unsigned)a.P, C::THREADS, (size_t)C::SMEM, s, ma, mb, a));
 }
 
 template <int DT>
@@ -113,11 +111,12 @@ FBArgs fb_args(int64_t M, int64_t N, int64_t K, const void* sa, const void* sw) 
 
 // ------------------------------------------------------------------ few tokens
 
-// Up to this many tokens (dense), or rows of an expert on average, the few-token kernel runs.
-constexpr int64_t kSmallTokens = 128;
-constexpr int64_t kSmallRows = 48;
-// From this many rows of an expert on average, pairs of CTAs take 256 of them at once.
-constexpr int64_t kPairRows = 192;
+// The few-token kernel runs up to this many tokens (dense; 8192 x 8192: 32 tokens 18.0 us against
+// 23.9, but 48 tokens 25.1 against 24.2; 5000 x 2064: 32 tokens 8.8 against 9.2, 48 tokens 14.1
+// against 9.2), or this many rows of an expert on average (64 experts of 2048 x 1024: 8 rows 86 us
+// against 95, 12 rows 101 against 96).
+constexpr int64_t kSmallTokens = 32;
+constexpr int64_t kSmallRows = 10;
 
 template <int BT, int KIND, int DT>
 apex_status_t launch_fs(const CUtensorMap& mw, const CUtensorMap& mx, const FBArgs& b,
@@ -143,30 +142,28 @@ apex_status_t fb_dense_t(int64_t M, int64_t N, int64_t K, const void* a_codes, c
                          FBArgs a, bool early, cudaStream_t s) {
   const int sms = dev_info().sms;
   if (M <= kSmallTokens) {
-    const int bt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int bt = M <= 16 ? 16 : 32;
     CUtensorMap ma, mb;
     if (!make_codes3_map(&mb, w_codes, 1, N, K, 128) || !make_expanded_map(&ma, a_codes, M, K, bt))
       return APEX_ERR_CUDA;
     a.tiles_m = (int)ceil_div(M, bt);
     a.tiles_n = a.NB;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    if (bt == 16) return launch_fs<16, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
-    if (bt == 32) return launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
-    return launch_fs<64, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
+    return bt == 16 ? launch_fs<16, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s)
+                    : launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
   }
   if (ceil_div(M, 128) * ceil_div(N, 128) >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
-  // 256 x 256 by pairs of CTAs where their tiles fill the GPU, else 256 x 128, else 128 x 128
-  auto tiles = [&](int bm, int bn) {
-    a.tiles_m = (int)ceil_div(M, bm);
-    a.tiles_n = (int)ceil_div(N, bn);
-    return (int64_t)a.tiles_m * a.tiles_n;
-  };
-  if (int64_t t = tiles(256, 256); 2 * t >= sms)
-    return launch_fb<256, 2, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
-  if (int64_t t = tiles(256, 128); 4 * t >= sms && M > 128)
-    return launch_fb<128, 2, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
-  const int64_t t = tiles(128, 128);
-  return launch_fb<128, 1, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, t, s);
+  // 128 x 256 tiles or 128 x 128: the wider ones take about 1.6 times as long (0.48 and 0.3 us a
+  // K-group), so whichever finishes its rounds over the SMs first (512 x 8192 x 8192: 39 against
+  // 50 us, 256 x 8192 x 8192: 37 against 26)
+  a.tiles_m = (int)ceil_div(M, 128);
+  const int64_t wide = a.tiles_m * ceil_div(N, 256), narrow = a.tiles_m * ceil_div(N, 128);
+  if (8 * ceil_div(wide, sms) <= 5 * ceil_div(narrow, sms)) {
+    a.tiles_n = (int)ceil_div(N, 256);
+    return launch_fb<256, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, wide, s);
+  }
+  a.tiles_n = (int)ceil_div(N, 128);
+  return launch_fb<128, apex::FB_DENSE, DT>(a_codes, M, w_codes, 1, a, narrow, s);
 }
 
 // early: the activations' quantizer of the same call is the launch before this one.
@@ -195,20 +192,15 @@ apex_status_t fb_experts(const void* codes, int64_t rows, const void* w_codes, F
   auto most_tiles = [&](int64_t bm, int64_t tiles_n) { return (experts + S / bm) * tiles_n; };
   if (most_tiles(16, a.NB) >= (1ll << 31) - 4096) return APEX_ERR_UNSUPPORTED;
   if (moe_small(S, a.E)) {
-    const int bt = S <= experts * 12 ? 16 : 32;
     CUtensorMap ma, mb;
     if (!make_codes3_map(&mb, w_codes, Z, N, K, 128) ||
-        !make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : bt))
+        !make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : 16))
       return APEX_ERR_CUDA;
     a.tiles_n = a.NB;
-    return bt == 16 ? launch_fs<16, KIND, DT>(mb, ma, a, most_tiles(16, a.NB), true, s)
-                    : launch_fs<32, KIND, DT>(mb, ma, a, most_tiles(32, a.NB), true, s);
+    return launch_fs<16, KIND, DT>(mb, ma, a, most_tiles(16, a.NB), true, s);
   }
   a.tiles_n = KIND == apex::FB_UP ? a.NB : (int)ceil_div(N, 256);
-  // pairs of CTAs take 256 rows of an expert at once: not worth it under about that many
-  if (S >= experts * kPairRows)
-    return launch_fb<256, 2, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(256, a.tiles_n), s);
-  return launch_fb<256, 1, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(128, a.tiles_n), s);
+  return launch_fb<256, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(128, a.tiles_n), s);
 }
 
 struct MoeWork {   // byte offsets into the workspace of apex_moe_mlp_fp8_block

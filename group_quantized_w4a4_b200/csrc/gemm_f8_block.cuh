@@ -20,11 +20,7 @@
 // Tile: 128 tokens (MMA M) x BN weight rows (MMA N), one K-group per pipeline stage, both
 // operands by TMA with 128-byte swizzle; the group's partial goes to one of 512 / BN
 // tensor-memory slots, which the epilogue drains while the next groups' MMAs fill the others.
-// CG = 2: the CTAs of a cluster of two compute 256 tokens x BN together (tcgen05
-// cta_group::2): each loads its own 128 tokens and half of the weight rows, which the tensor
-// cores read from both.  A 128 x 256 tile alone needs 48 KB of operands a K-group from L2, and
-// that stream (10.7 TB/s at 4096 x 8192 x 8192) is what bounded it; a pair needs 32 KB a CTA.
-// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA (of the even CTA),
+// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA,
 // warps 2, 3 scales (global memory to a ring in shared memory, four K-groups of the 128 tokens
 // and of the tile's two weight blocks at a time, and which tile they are of), warps 4..11 epilogue (warp w: lanes
 // 32*(w%4).., half (w-4)/4 of the columns).  With its 128 accumulators and 64 partials in
@@ -62,13 +58,11 @@ struct FBArgs {
 
 constexpr int kMaxExperts = 512;
 
-template <int BN, int CG>
+template <int BN>
 struct FBCfg {
-  static constexpr int BM = 128 * CG;              // rows of a tile, 128 of them in each CTA
-  static constexpr int BROWS = BN / CG;            // weight rows that a CTA loads
-  static constexpr int BOX = BROWS < 128 ? BROWS : 128;
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BROWS * 128;
+  static constexpr int BM = 128;
+  static constexpr int A_BYTES = BM * 128;
+  static constexpr int B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NS = 168 * 1024 / STAGE;
   static constexpr int SLOTS = 512 / BN;
@@ -206,13 +200,12 @@ __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restri
   }
 }
 
-template <int BN, int CG, int KIND, int DT>
-__global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
+template <int BN, int KIND, int DT>
+__global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     f8_block_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB, const FBArgs args) {
-  using C = FBCfg<BN, CG>;
+  using C = FBCfg<BN>;
   using D = DTraits<DT>;
-  constexpr bool PAIR = CG == 2;
   constexpr bool EXPERTS = KIND != FB_DENSE;
   static_assert(KIND != FB_UP || BN == 256, "gate and up halves of 128");
   extern __shared__ uint8_t smem_raw[];
@@ -237,8 +230,6 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint64_t lim = args.wait_ns;
   const int G = args.G;
-  const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;   // CTA of the pair; the even one leads
-  const int t_first = (int)blockIdx.x / CG, t_step = args.P / CG;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
@@ -247,7 +238,7 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), CG * C::EPI_WARPS);
+      mbar_init(smem_u32(&tempty[i]), C::EPI_WARPS);
     }
     for (int i = 0; i < C::SR; ++i) {
       mbar_init(smem_u32(&sfull[i]), 64);
@@ -261,13 +252,8 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(s_tmem), 512);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(s_tmem), 512);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
   }
   if constexpr (EXPERTS) {
     grid_dep_wait();   // the offsets
@@ -275,10 +261,6 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) {   // both CTAs' barriers and tensor memory exist
-    cluster_arrive();
-    cluster_wait();
-  }
   tc_fence_after();
   grid_dep_launch();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(s_tmem);
@@ -307,50 +289,40 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
       if constexpr (!EXPERTS) grid_dep_wait();
       int it = 0, last = -1;
       bool ok = true;
-      for (int t = t_first; ok && t < T; t += t_step) {
+      for (int t = blockIdx.x; ok && t < T; t += args.P) {
         const ExpertTile x = tile_of(t);
         for (int g = 0; g < G; ++g, ++it) {
           const int st = it % C::NS;
           ok = mbar_wait_warp(smem_u32(&empty[st]), ((uint32_t)(it / C::NS) & 1u) ^ 1u, lim, abort_flag);
           if (!ok) break;
-          // the bytes of both CTAs of a pair are counted on the even one's barrier
-          const uint32_t fb = PAIR ? cluster_map(smem_u32(&full[st]), 0u) : smem_u32(&full[st]);
+          const uint32_t fb = smem_u32(&full[st]);
           const uint32_t a_dst = smem_u32(smem + st * C::STAGE);
           const uint32_t b_dst = a_dst + C::A_BYTES;
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[st]), CG * C::STAGE);
-            if constexpr (PAIR) tma_load_2d_pair(a_dst, &tmA, fb, g * 128, x.row0 + 128 * rank);
-            else tma_load_2d(a_dst, &tmA, fb, g * 128, x.row0);
+            mbar_arrive_expect_tx(fb, C::STAGE);
+            tma_load_2d(a_dst, &tmA, fb, g * 128, x.row0);
 #pragma unroll
-            for (int h = 0; h < C::BROWS / C::BOX; ++h) {
+            for (int h = 0; h < BN / 128; ++h) {
               // FB_UP: 128 gate rows, then the 128 up rows of the same outputs
-              const int half = PAIR ? rank : h;
-              const int n = KIND == FB_UP ? x.tn * 128 : x.tn * BN + half * C::BOX;
-              const int z = KIND == FB_UP ? 2 * x.e + half : x.e;
-              if constexpr (PAIR) tma_load_3d_pair(b_dst + h * C::BOX * 128, &tmB, fb, g * 128, n, z);
-              else tma_load_3d(b_dst + h * C::BOX * 128, &tmB, fb, g * 128, n, z);
+              const int n = KIND == FB_UP ? x.tn * 128 : x.tn * BN + h * 128;
+              const int z = KIND == FB_UP ? 2 * x.e + h : x.e;
+              tma_load_3d(b_dst + h * 128 * 128, &tmB, fb, g * 128, n, z);
             }
           }
           __syncwarp();
           last = it;
         }
       }
-      // never leave the CTA with bulk copies in flight (the even CTA's barriers count the
-      // other's copies too, and the pair leaves together; the other CTA, after a wait that gave
-      // up, lets its last copies land)
-      if (rank == 0) {
-        for (int s = (last - C::NS + 1 > 0 ? last - C::NS + 1 : 0); s <= last; ++s)
-          mbar_wait(smem_u32(&full[s % C::NS]), (uint32_t)(s / C::NS) & 1u, lim, never);
-      } else if (!ok) {
-        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-      }
+      // never leave the CTA with bulk copies in flight
+      for (int s = (last - C::NS + 1 > 0 ? last - C::NS + 1 : 0); s <= last; ++s)
+        mbar_wait(smem_u32(&full[s % C::NS]), (uint32_t)(s / C::NS) & 1u, lim, never);
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc = idesc_e4m3(C::BM, BN);
       int it = 0;
-      bool ok = rank == 0;
-      for (int t = t_first; ok && t < T; t += t_step) {
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < T; t += args.P) {
         for (int g = 0; g < G; ++g, ++it) {
           const int st = it % C::NS, sl = it % C::SLOTS;
           ok = mbar_wait2_warp(smem_u32(&full[st]), (uint32_t)(it / C::NS) & 1u,
@@ -364,43 +336,31 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
             const uint64_t b0 = smem_desc_k_sw128(a_at + C::A_BYTES);
             const uint32_t d = tbase + sl * BN;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {   // 32 codes of K per MMA (+2 in 16-byte units)
-              if constexpr (PAIR)
-                umma_f8_ss_pair(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
-              else
-                umma_f8_ss(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
-            }
-            if constexpr (PAIR) {
-              umma_commit_pair(smem_u32(&empty[st]));
-              umma_commit_pair(smem_u32(&tfull[sl]));
-            } else {
-              umma_commit(smem_u32(&empty[st]));
-              umma_commit(smem_u32(&tfull[sl]));
-            }
+            for (int j = 0; j < 4; ++j)   // 32 codes of K per MMA (+2 in 16-byte units)
+              umma_f8_ss(d, a0 + (uint64_t)(2 * j), b0 + (uint64_t)(2 * j), idesc, j > 0 ? 1u : 0u);
+            umma_commit(smem_u32(&empty[st]));
+            umma_commit(smem_u32(&tfull[sl]));
           }
           __syncwarp();
         }
       }
-      if (elect_one() && rank == 0) {   // arrives in both CTAs of a pair
-        if constexpr (PAIR) umma_commit_pair(smem_u32(mma_done));
-        else umma_commit(smem_u32(mma_done));
-      }
+      if (elect_one()) umma_commit(smem_u32(mma_done));
       __syncwarp();
       mbar_wait(smem_u32(mma_done), 0u, lim, never);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- scales
       if constexpr (!EXPERTS) grid_dep_wait();
-      const int i0 = threadIdx.x - 64;          // rows i0 and i0 + 64 of this CTA's 128
+      const int i0 = threadIdx.x - 64;          // rows i0 and i0 + 64 of the tile's 128
       const bool s_vec = args.s_vec != 0;
       int sb = 0, tno = 0;
       bool ok = true;
-      for (int t = t_first; ok && t < T; t += t_step, ++tno) {
+      for (int t = blockIdx.x; ok && t < T; t += args.P, ++tno) {
         const ExpertTile x = tile_of(t);
         const float* sa[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int r = 128 * rank + i0 + 64 * i;
+          const int r = i0 + 64 * i;
           sa[i] = nullptr;
           if (r < x.rows) sa[i] = args.sa + (size_t)(x.row0 + r) * G;
         }
@@ -436,8 +396,7 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     if constexpr (!EXPERTS) grid_dep_wait();
     const int lq = warp & 3;                  // tensor-memory lane quarter of this warp
     const int half = (warp - 4) >> 2;
-    const int row = 32 * lq + lane;           // token of this CTA's 128
-    const int trow = 128 * rank + row;        // token of the tile
+    const int row = 32 * lq + lane;           // token of the tile
     const uint32_t t_lane = (uint32_t)(32 * lq) << 16;
     constexpr int NCH = C::CPT / 32;
     // tensor-memory column of this thread's 32-column chunk cc: for FB_UP its 64 gate
@@ -449,13 +408,13 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
     float2 acc[C::CPT / 2];
     bool ok = true;
     int it = 0, sb = 0, tno = 0;
-    for (int t = t_first; ok && t < T; t += t_step, ++tno) {
+    for (int t = blockIdx.x; ok && t < T; t += args.P, ++tno) {
       // the tile's first scale block comes with its description
       ok = mbar_wait_warp(smem_u32(&sfull[sb % C::SR]), (uint32_t)(sb / C::SR) & 1u, lim, abort_flag);
       const int4 xd = ok ? s_tile[tno % C::TR] : make_int4(0, 0, 0, 0);
       const int x_row0 = xd.y, x_rows = xd.z, x_tn = xd.w;
-      const bool live = trow < x_rows;
-      const int s = x_row0 + (live ? trow : 0);
+      const bool live = row < x_rows;
+      const int s = x_row0 + (live ? row : 0);
       int out_row = live ? s : -1;
       if constexpr (KIND == FB_DOWN) {   // (checked where it is used, when it has arrived)
         if (live) out_row = __ldg(args.order + s);
@@ -517,10 +476,7 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
           if (cc == NCH - 2) {   // every load of the slot has completed
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) {
-              if constexpr (PAIR) mbar_arrive_cluster(cluster_map(smem_u32(&tempty[sl]), 0u));
-              else mbar_arrive(smem_u32(&tempty[sl]));
-            }
+            if (elect_one()) mbar_arrive(smem_u32(&tempty[sl]));
           }
         }
         ++it;
@@ -630,14 +586,9 @@ __global__ void __launch_bounds__(FBCfg<BN, CG>::THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) {   // neither CTA's memory is in use by the other any more
-    cluster_arrive();
-    cluster_wait();
-  }
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (PAIR) tmem_dealloc_pair(tbase, 512);
-    else tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, 512);
   }
 }
 

@@ -2,10 +2,10 @@
 // kinds, operands and results of gemm_f8_block.cuh.
 //
 // Bound: the weights' stream from HBM.  The 128 tensor-memory lanes hold weight rows and the
-// tokens are the MMA's N (BT = 16, 32 or 64), so a tile wastes nothing on absent tokens.  A
+// tokens are the MMA's N (BT = 16 or 32), so a tile wastes little on absent tokens.  A
 // pipeline stage is one K-group of 128 weight rows (16 KB) and its tokens; for FB_UP the gate
-// and up rows of an output block alternate as stages.  Two CTAs share an SM (one, for 64
-// tokens), each with its ring of stages, so that one streams while the other starts or ends.
+// and up rows of an output block alternate as stages.  Two CTAs share an SM, each with its ring
+// of stages, so that one streams while the other starts or ends.
 //
 // K is split over the S CTAs of a thread-block cluster when there are too few tiles: every
 // CTA sends its fp32 sums of BT / S tokens to each of the others (st.async, counted on an
@@ -34,7 +34,7 @@ struct FSArgs {
 template <int BT, int KIND>
 struct FSCfg {
   static constexpr int HALVES = KIND == FB_UP ? 2 : 1;
-  static constexpr int CTAS_PER_SM = BT == 64 ? 1 : 2;
+  static constexpr int CTAS_PER_SM = 2;
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = BT * 128;
   static constexpr int STAGE = W_BYTES + X_BYTES;
@@ -42,7 +42,7 @@ struct FSCfg {
   static constexpr int SC = 4 * 2 * 4 * BT * 4;         // [warp][2][4 groups][BT] token scales
   static constexpr int CUM = KIND == FB_DENSE ? 0 : (kMaxExperts + 4) * 4;
   static constexpr int FIXED = RECV + SC + CUM + 4 * BT * 4 + 512 + 1024;
-  static constexpr int BUDGET = CTAS_PER_SM == 2 ? 113 * 1024 : 220 * 1024;
+  static constexpr int BUDGET = 113 * 1024;
   static constexpr int NS = (BUDGET - FIXED) / STAGE < 8 ? (BUDGET - FIXED) / STAGE : 8;
   static constexpr int SLOTS = 256 / BT < 8 ? 256 / BT : 8;   // partials of BT columns
   static constexpr int TMEM_COLS = SLOTS * BT;
@@ -74,10 +74,9 @@ __device__ __forceinline__ void tmem_ld_tokens(uint32_t taddr, uint32_t (&v)[BT]
     tmem_ld16_nowait(taddr, v);
     tmem_ld_wait16(v);
   } else {
-#pragma unroll
-    for (int c = 0; c < BT / 32; ++c) tmem_ld32_nowait(taddr + 32 * c, v + 32 * c);
-#pragma unroll
-    for (int c = 0; c < BT / 32; ++c) tmem_ld_wait32(v + 32 * c);
+    static_assert(BT == 32, "16 or 32 tokens");
+    tmem_ld32_nowait(taddr, v);
+    tmem_ld_wait32(v);
   }
 }
 

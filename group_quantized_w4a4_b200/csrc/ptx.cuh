@@ -283,32 +283,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, uint3
       : "memory");
 }
 
-// The same loads by one CTA of a pair (cta_group::2): dst in this CTA's shared memory, the bytes
-// counted on `bar`, a shared::cluster address of a barrier of either CTA.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar,
-                                                 int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, uint32_t bar,
-                                                 int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-// Arrive at a barrier of another CTA of the cluster (rbar: a shared::cluster address), to hand
-// over tensor memory (tc_fence_before orders its reads): no ordinary memory is published, so
-// the arrive does not release at cluster scope, which would wait for every earlier access of
-// the thread (569 instead of 338 us at 4096 x 8192 x 8192).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t rbar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(rbar) : "memory");
-}
-
 // Order this thread's generic-proxy shared-memory writes before later async-proxy reads
 // (tensor core operand fetches).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -379,40 +353,6 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
                : "memory");
-}
-
-// The same for a pair of CTAs (cta_group::2, a cluster's even rank and the next one).  One warp
-// of each CTA allocates and frees; the even CTA issues the MMAs, whose A rows and D lanes are
-// split between the CTAs' memories by M halves and whose B rows by N halves, at the same
-// addresses in both; a commit arrives at the barrier of the same address in both CTAs.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void umma_f8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b16 m;\n\t"
-      "mov.b16 m, 3;\n\t"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], m;\n\t}" ::"r"(bar)
-      : "memory");
 }
 
 // 32 lanes x 16 columns of 32-bit, one lane per thread; waits for completion.
