@@ -141,13 +141,14 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const NormArgs a
   }
 }
 
-// out[t] = sum_j weights[t,j] * y[t * k + j] over the choices with an id in [0, E), in the
-// order of j, in fp32.
+// out[t] = sum_j weights[t,j] * y[row of t * k + j] over the choices with an id in [0, E), in the
+// order of j, in fp32; the row is the flat index itself, or slot_of[it].
 template <int DT>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y,
                                                       const float* __restrict__ weights,
-                                                      const int32_t* __restrict__ ids, int T, int H,
-                                                      int k, int E, void* __restrict__ out) {
+                                                      const int32_t* __restrict__ ids,
+                                                      const int32_t* __restrict__ slot_of, int T,
+                                                      int H, int k, int E, void* __restrict__ out) {
   using D = DTraits<DT>;
   grid_dep_wait();
   grid_dep_launch();
@@ -167,8 +168,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y
         w[u] = 0.0f;
         r[u] = make_uint4(0u, 0u, 0u, 0u);
         if (id >= 0 && id < E) {
-          w[u] = __ldg(weights + t * k + j0 + u);
-          r[u] = raw8(y, (size_t)(t * k + j0 + u) * H + c);
+          int row = (int)(t * k) + j0 + u;
+          if (slot_of) row = __ldg(slot_of + row);
+          if (row >= 0 && row < T * k) {   // (no order's slots lead out of y)
+            w[u] = __ldg(weights + t * k + j0 + u);
+            r[u] = raw8(y, (size_t)row * H + c);
+          }
         }
       }
 #pragma unroll

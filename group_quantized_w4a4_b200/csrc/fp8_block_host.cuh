@@ -39,6 +39,23 @@ bool make_codes3_map(CUtensorMap* map, const void* base, int64_t Z, int64_t rows
   return r == CUDA_SUCCESS;
 }
 
+// 2-D map over outputs [rows][cols] of `size`-byte elements, written in boxes of 32 rows x
+// box_cols columns from shared memory with that many bytes' swizzle.
+bool make_out_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int size,
+                  int box_cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, 32u};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = fn(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                  base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_cols * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 template <typename F>
 cudaError_t set_smem(F kern, int bytes, int* attr_dev) {   // once per device and kernel
   int dev = 0;
@@ -59,13 +76,20 @@ apex_status_t launch_fb(const void* a_codes, int64_t a_rows, const void* w_codes
   auto kern = apex::f8_block_gemm_kernel<BN, KIND, DT>;
   static thread_local int attr_dev = -1;
   if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, my;
   if (!make_expanded_map(&ma, a_codes, a_rows, a.K, 128) ||
       !make_codes3_map(&mb, w_codes, Z, a.N, a.K, 128))
     return APEX_ERR_CUDA;
+  if (KIND == apex::FB_UP) {
+    if (!make_out_map(&my, a.hq, a_rows, a.N, 1, 64)) return APEX_ERR_CUDA;
+  } else if (a.y_map) {
+    if (!make_out_map(&my, a.y, a_rows, a.N, 2, 64)) return APEX_ERR_CUDA;
+  } else {
+    my = ma;   // never used
+  }
   const int64_t most = dev_info().sms;
   a.P = (int)(tiles < most ? tiles : most);
-  return launched(launch_pdl(kern, (unsigned)a.P, C::THREADS, (size_t)C::SMEM, s, ma, mb, a));
+  return launched(launch_pdl(kern, (unsigned)a.P, C::THREADS, (size_t)C::SMEM, s, ma, mb, my, a));
 }
 
 template <int DT>
@@ -120,13 +144,14 @@ constexpr int64_t kSmallRows = 10;
 
 template <int BT, int KIND, int DT>
 apex_status_t launch_fs(const CUtensorMap& mw, const CUtensorMap& mx, const FBArgs& b,
-                        int64_t tiles, bool early, cudaStream_t s) {
+                        const int32_t* order, int64_t tiles, bool early, cudaStream_t s) {
   using C = apex::FSCfg<BT, KIND>;
   auto kern = apex::f8_small_gemm_kernel<BT, KIND, DT>;
   static thread_local int attr_dev = -1;
   if (set_smem(kern, C::SMEM, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
   apex::FSArgs a;
   a.b = b;
+  a.order = order;
   a.early = early ? 1 : 0;
   // K split over a cluster while that leaves every CTA two groups and all CTAs resident
   const int64_t room = (int64_t)dev_info().sms * C::CTAS_PER_SM;
@@ -149,8 +174,8 @@ apex_status_t fb_dense_t(int64_t M, int64_t N, int64_t K, const void* a_codes, c
     a.tiles_m = (int)ceil_div(M, bt);
     a.tiles_n = a.NB;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    return bt == 16 ? launch_fs<16, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s)
-                    : launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, tiles, early, s);
+    return bt == 16 ? launch_fs<16, apex::FB_DENSE, DT>(mb, ma, a, nullptr, tiles, early, s)
+                    : launch_fs<32, apex::FB_DENSE, DT>(mb, ma, a, nullptr, tiles, early, s);
   }
   if (ceil_div(M, 128) * ceil_div(N, 128) >= (1ll << 31) - sms) return APEX_ERR_UNSUPPORTED;
   // 128 x 256 tiles or 128 x 128: the wider ones take about 1.6 times as long (0.48 and 0.3 us a
@@ -172,7 +197,7 @@ apex_status_t fb_dense(int64_t M, int64_t N, int64_t K, const void* a_codes, con
                        bool early, cudaStream_t s) {
   FBArgs a = fb_args(M, N, K, a_scales, w_scales);
   a.y = y;
-  a.y_vec = N % 8 == 0 && aligned(y, 16);
+  a.y_map = N % 8 == 0 && aligned(y, 16);
   return dtype == APEX_DTYPE_F16 ? fb_dense_t<apex::DT_F16>(M, N, K, a_codes, w_codes, a, early, s)
                                  : fb_dense_t<apex::DT_BF16>(M, N, K, a_codes, w_codes, a, early, s);
 }
@@ -184,7 +209,7 @@ bool moe_small(int64_t S, int64_t E) { return S <= (S < E ? S : E) * kSmallRows;
 // of the activations' codes; the launch before this one is the one that writes them.
 template <int KIND, int DT>
 apex_status_t fb_experts(const void* codes, int64_t rows, const void* w_codes, FBArgs a,
-                         cudaStream_t s) {
+                         const int32_t* order, cudaStream_t s) {
   const int64_t S = a.slots, N = a.N, K = a.K;
   const int64_t Z = (KIND == apex::FB_UP ? 2 : 1) * (int64_t)a.E;
   const int64_t experts = S < a.E ? S : a.E;
@@ -197,14 +222,14 @@ apex_status_t fb_experts(const void* codes, int64_t rows, const void* w_codes, F
         !make_expanded_map(&ma, codes, rows, K, KIND == apex::FB_UP ? 1 : 16))
       return APEX_ERR_CUDA;
     a.tiles_n = a.NB;
-    return launch_fs<16, KIND, DT>(mb, ma, a, most_tiles(16, a.NB), true, s);
+    return launch_fs<16, KIND, DT>(mb, ma, a, order, most_tiles(16, a.NB), true, s);
   }
   a.tiles_n = KIND == apex::FB_UP ? a.NB : (int)ceil_div(N, 256);
   return launch_fb<256, KIND, DT>(codes, rows, w_codes, Z, a, most_tiles(128, a.tiles_n), s);
 }
 
 struct MoeWork {   // byte offsets into the workspace of apex_moe_mlp_fp8_block
-  size_t xq, xs, pq, ps, hq, hs, y, total;
+  size_t xq, xs, pq, ps, slot, hq, hs, y, total;
 };
 MoeWork moe_work(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   MoeWork w;
@@ -212,9 +237,11 @@ MoeWork moe_work(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   w.xq = 0;
   w.xs = w.xq + pad256((size_t)T * H);
   w.pq = w.xs + pad256((size_t)T * ceil_div(H, 128) * 4);
-  // the tokens' rows by slot, where they are not gathered
-  w.ps = w.pq + (moe_small((int64_t)S, E) ? 0 : pad256(S * H));
-  w.hq = w.ps + (moe_small((int64_t)S, E) ? 0 : pad256(S * ceil_div(H, 128) * 4));
+  // the tokens' rows by slot and the flat indices' slots, where rows are not gathered
+  const bool small = moe_small((int64_t)S, E);
+  w.ps = w.pq + (small ? 0 : pad256(S * H));
+  w.slot = w.ps + (small ? 0 : pad256(S * ceil_div(H, 128) * 4));
+  w.hq = w.slot + (small ? 0 : pad256(S * 4));
   w.hs = w.hq + pad256(S * I);
   w.y = w.hs + pad256(S * ceil_div(I, 128) * 4);
   w.total = w.y + pad256(S * H * 2);
@@ -488,42 +515,43 @@ apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H,
     a.slots = (int)S;
     a.top_k = k;
     a.offsets = static_cast<const int32_t*>(offsets_i32);
-    a.order = static_cast<const int32_t*>(order_i32);
     return a;
   };
+  const int32_t* order = static_cast<const int32_t*>(order_i32);
   const bool small = moe_small(S, E);
   if (!small) {
     st = launched(launch_pdl(apex::f8_permute_kernel, grid_for(S * 32, 256, 8), 256, 0, s,
                              (const uint8_t*)(ws + w.xq), (const float*)(ws + w.xs),
-                             static_cast<const int32_t*>(order_i32), (int)S, (int)k, (int)H,
-                             (int)ceil_div(H, 128), ws + w.pq,
-                             reinterpret_cast<float*>(ws + w.ps)));
+                             order, (int)S, (int)k, (int)H, (int)ceil_div(H, 128), ws + w.pq,
+                             reinterpret_cast<float*>(ws + w.ps),
+                             reinterpret_cast<int32_t*>(ws + w.slot)));
     if (st != APEX_OK) return st;
   }
   FBArgs up = with_experts(fb_args(small ? T : S, I, H, ws + (small ? w.xs : w.ps), w13_scales));
   up.hq = ws + w.hq;
   up.hs = reinterpret_cast<float*>(ws + w.hs);
   st = fb_experts<apex::FB_UP, apex::DT_BF16>(ws + (small ? w.xq : w.pq), small ? T : S, w13_codes,
-                                              up, s);
+                                              up, order, s);
   if (st != APEX_OK) return st;
 
   FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales));
   down.y = ws + w.y;
-  down.y_vec = 1;
+  down.y_map = 1;
   const bool f16 = dtype == APEX_DTYPE_F16;
-  st = f16 ? fb_experts<apex::FB_DOWN, apex::DT_F16>(ws + w.hq, S, w2_codes, down, s)
-           : fb_experts<apex::FB_DOWN, apex::DT_BF16>(ws + w.hq, S, w2_codes, down, s);
+  st = f16 ? fb_experts<apex::FB_DOWN, apex::DT_F16>(ws + w.hq, S, w2_codes, down, order, s)
+           : fb_experts<apex::FB_DOWN, apex::DT_BF16>(ws + w.hq, S, w2_codes, down, order, s);
   if (st != APEX_OK) return st;
 
   const unsigned blocks = grid_for(T * (H / 8), 256, 16);
+  const int32_t* slot_of = small ? nullptr : reinterpret_cast<const int32_t*>(ws + w.slot);
   return launched(f16 ? launch_pdl(apex::combine_kernel<apex::DT_F16>, blocks, 256, 0, s,
                                    (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
-                                   static_cast<const int32_t*>(ids_i32), (int)T, (int)H, (int)k,
-                                   (int)E, y)
+                                   static_cast<const int32_t*>(ids_i32), slot_of, (int)T, (int)H,
+                                   (int)k, (int)E, y)
                       : launch_pdl(apex::combine_kernel<apex::DT_BF16>, blocks, 256, 0, s,
                                    (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
-                                   static_cast<const int32_t*>(ids_i32), (int)T, (int)H, (int)k,
-                                   (int)E, y));
+                                   static_cast<const int32_t*>(ids_i32), slot_of, (int)T, (int)H,
+                                   (int)k, (int)E, y));
 }
 
 apex_status_t apex_block_norm(const void* x, int32_t dtype, int64_t T, int64_t H,

@@ -15,14 +15,14 @@
 //             128 up rows.  The rows are slots: f8_permute_kernel has copied each token's
 //             codes to the slots of its choices (fetching scattered rows here by TMA gathers of
 //             four took 1.5 us a K-group, three times the products).
-//   FB_DOWN   h . W^T of each slot's expert, written to row order[s] (token-major).
+//   FB_DOWN   h . W^T of each slot's expert, by slot.
 //
 // Tile: 128 tokens (MMA M) x BN weight rows (MMA N), one K-group per pipeline stage, both
 // operands by TMA with 128-byte swizzle; the group's partial goes to one of 512 / BN
 // tensor-memory slots, which the epilogue drains while the next groups' MMAs fill the others.
-// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA,
-// warps 2, 3 scales (global memory to a ring in shared memory, four K-groups of the 128 tokens
-// and of the tile's two weight blocks at a time, and which tile they are of), warps 4..11 epilogue (warp w: lanes
+// Roles (384 threads, one persistent CTA per SM): warp 0 TMA, warp 1 MMA, warps 2, 3 scales
+// (global memory to a ring in shared memory, four K-groups of the 128 tokens and of the tile's
+// two weight blocks at a time, and which tile they are of), warps 4..11 epilogue (warp w: lanes
 // 32*(w%4).., half (w-4)/4 of the columns).  With its 128 accumulators and 64 partials in
 // flight an epilogue thread has no registers for scales on their way from memory: loaded
 // there, every fourth group waited 1,100 cycles for them.
@@ -45,14 +45,13 @@ struct FBArgs {
   // experts (FB_UP, FB_DOWN): slots = T * k rows at most, grouped by expert
   int E, slots, top_k;
   const int32_t* offsets;   // [E + 1]
-  const int32_t* order;     // [slots]
   const float* sa;          // [rows][G]
   const float* sw;          // [E (x 2 for FB_UP)][NB][G]
   void* y;                  // [rows][N]
   uint8_t* hq;              // FB_UP: codes [slots][N] and scales [slots][NB]
   float* hs;
   int s_vec;                // scale rows readable as 16-byte blocks of 4 groups
-  int y_vec;                // output rows writable as 16-byte vectors
+  int y_map;                // rows of y are 16-byte multiples: tmY describes them
   unsigned long long wait_ns;
 };
 
@@ -74,8 +73,9 @@ struct FBCfg {
   static constexpr int CPT = BN / 2;   // partials per epilogue thread
   static constexpr int SR = 4;                     // ring of scale blocks (4 K-groups each)
   static constexpr int SC_BLOCK = (128 + 2) * 16;  // [128 tokens, 2 weight blocks][4 groups]
-  static constexpr int OFF_ST = NS * STAGE;        // 4 KB a warp: outputs on their way to rows
-  static constexpr int OFF_SC = OFF_ST + EPI_WARPS * 4096;
+  static constexpr int ST_WARP = CPT * 64;         // a warp's 32 rows of outputs on their way
+  static constexpr int OFF_ST = NS * STAGE;
+  static constexpr int OFF_SC = OFF_ST + EPI_WARPS * ST_WARP;
   static constexpr int OFF_CUM = OFF_SC + SR * SC_BLOCK;           // [kMaxExperts + 1] ints
   static constexpr int OFF_AMAX = OFF_CUM + (kMaxExperts + 4) * 4;  // [2][2][128] words
   static constexpr int TR = 8;                     // ring of tile descriptions, 16 bytes each
@@ -168,7 +168,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * rcp_approx(1.0f + __expf(-g)) * u;
 }
 
-// Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k.
+// Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k, and
+// slot_of[order[s]] = s.
 // Bound: the copy itself, a byte read (from L2, k times) and written per element.  A warp per
 // slot.
 __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restrict__ codes,
@@ -176,7 +177,8 @@ __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restri
                                                          const int32_t* __restrict__ order,
                                                          int slots, int top_k, int K, int G,
                                                          uint8_t* __restrict__ to_codes,
-                                                         float* __restrict__ to_scales) {
+                                                         float* __restrict__ to_scales,
+                                                         int32_t* __restrict__ slot_of) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restri
     const int f = __ldg(order + s);
     if (f < 0 || f >= slots) continue;   // no choice
     const int t = f / top_k;
+    if (lane == 0) slot_of[f] = s;
     const uint4* src = reinterpret_cast<const uint4*>(codes + (size_t)t * K);
     uint4* dst = reinterpret_cast<uint4*>(to_codes + (size_t)s * K);
     for (int c0 = 0; c0 < chunks; c0 += 128) {   // four loads in flight
@@ -203,7 +206,8 @@ __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restri
 template <int BN, int KIND, int DT>
 __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
     f8_block_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                         const __grid_constant__ CUtensorMap tmB, const FBArgs args) {
+                         const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmY, const FBArgs args) {
   using C = FBCfg<BN>;
   using D = DTraits<DT>;
   constexpr bool EXPERTS = KIND != FB_DENSE;
@@ -415,10 +419,6 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
       const int x_row0 = xd.y, x_rows = xd.z, x_tn = xd.w;
       const bool live = row < x_rows;
       const int s = x_row0 + (live ? row : 0);
-      int out_row = live ? s : -1;
-      if constexpr (KIND == FB_DOWN) {   // (checked where it is used, when it has arrived)
-        if (live) out_row = __ldg(args.order + s);
-      }
 #pragma unroll
       for (int e = 0; e < C::CPT / 2; ++e) acc[e] = make_float2(0.0f, 0.0f);
       // The partials come in chunks of 32 columns, the next one's load in flight while one is
@@ -485,10 +485,16 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
           if (ok) load_block();
         }
       }
-      // The tile's outputs go through the warp's own 4 KB of shared memory (16-byte chunks,
-      // permuted so that neither side meets bank conflicts), so that a store writes whole
-      // 128-byte (FB_UP: 64-byte) lines of a few rows instead of 16 bytes of 32 rows.
-      uint8_t* stage = smem + C::OFF_ST + (warp - 4) * 4096;
+      // The tile's outputs go through the warp's own shared memory (16-byte chunks permuted as
+      // the 128-byte, FB_UP: 64-byte, swizzle of the output's map) and leave by bulk stores,
+      // which drain while the next tile is computed: the CTAs finish their tiles together, and
+      // plain stores of 64 KB from each then took 3,300 to 4,200 cycles, a quarter of a tile of
+      // eight K-groups.  Rows of the last, partly filled tile of an expert, which other rows
+      // follow, are stored one by one, and so are outputs no map can describe.
+      uint8_t* stage = smem + C::OFF_ST + (warp - 4) * C::ST_WARP;
+      if (elect_one()) bulk_wait_read();   // the last tile's
+      __syncwarp();
+      const bool whole = 32 * lq + 32 <= x_rows || KIND == FB_DENSE;
       if constexpr (KIND == FB_UP) {
         // h of this thread's 64 columns, the group's maximum with the thread that holds the
         // row's other 64, then the codes
@@ -521,58 +527,59 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
                 make_uint4(a.x, a.y, b.x, b.y);
           }
           if (half == 0 && live) args.hs[(size_t)s * args.NB + x_tn] = q.s;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2), c = lane & 3;
-            const int slot = __shfl_sync(0xffffffffu, out_row, r);
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-            if (slot >= 0 && n0 + c * 16 < args.N)   // N % 16 == 0
-              *reinterpret_cast<uint4*>(args.hq + (size_t)slot * args.N + n0 + c * 16) = v;
+          if (whole) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one() && n0 < args.N) {
+              tma_store_2d(&tmY, smem_u32(stage), n0, x_row0 + 32 * lq);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2), c = lane & 3;
+              if (32 * lq + r < x_rows && n0 + c * 16 < args.N)   // N % 16 == 0
+                *reinterpret_cast<uint4*>(args.hq + (size_t)(x_row0 + 32 * lq + r) * args.N + n0 + c * 16) =
+                    *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       } else if (ok) {
-        if (KIND == FB_DOWN && out_row >= args.slots) out_row = -1;
 #pragma unroll
-        for (int pass = 0; pass < C::CPT / 64; ++pass) {
+        for (int pass = 0; pass < C::CPT / 64; ++pass)
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float2* a = acc + pass * 32 + c * 4;
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(stage + pass * 4096 + lane * 128 + ((c ^ (lane & 7)) << 4)) =
                 make_uint4(D::pack(a[0].x, a[0].y), D::pack(a[1].x, a[1].y),
                            D::pack(a[2].x, a[2].y), D::pack(a[3].x, a[3].y));
           }
+        const int n0 = x_tn * BN + half * C::CPT;
+        if (whole && args.y_map) {
+          fence_proxy_async_smem();
           __syncwarp();
-          const int n = x_tn * BN + half * C::CPT + pass * 64 + (lane & 7) * 8;
-          uint4 v[8];
-          int to[8];
+          if (elect_one() && 32 * lq < x_rows) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            to[i] = __shfl_sync(0xffffffffu, out_row, r);
-            v[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            for (int pass = 0; pass < C::CPT / 64; ++pass)
+              if (n0 + pass * 64 < args.N)
+                tma_store_2d(&tmY, smem_u32(stage + pass * 4096), n0 + pass * 64, x_row0 + 32 * lq);
+            bulk_commit();
           }
-          if (args.y_vec) {   // N % 8 == 0
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (n < args.N && to[i] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<typename D::T*>(args.y) +
-                                          (size_t)to[i] * args.N + n) = v[i];
-          } else {
+        } else {
+          __syncwarp();
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              int row_to = to[0];
-              uint4 w4 = v[0];
-#pragma unroll
-              for (int u = 1; u < 8; ++u)
-                if (u == i) {
-                  row_to = to[u];
-                  w4 = v[u];
-                }
-              if (row_to < 0) continue;
-              uint16_t* dst = static_cast<uint16_t*>(args.y) + (size_t)row_to * args.N + n;
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          for (int i = 0; i < C::CPT / 8; ++i) {   // 4 rows of 64 columns each
+            const int pass = i >> 3, r = (i & 7) * 4 + (lane >> 3), c = lane & 7;
+            const int n = n0 + pass * 64 + c * 8;
+            if (32 * lq + r >= x_rows) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + pass * 4096 + r * 128 + ((c ^ (r & 7)) << 4));
+            uint16_t* dst = static_cast<uint16_t*>(args.y) + (size_t)(x_row0 + 32 * lq + r) * args.N + n;
+            if (args.y_map && n < args.N) {   // N % 8 == 0, 16-byte rows
+              *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (n + e < args.N) dst[e] = (uint16_t)((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
@@ -582,6 +589,8 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
         }
       }
     }
+    if (elect_one()) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();

@@ -1,6 +1,9 @@
 // gemm_f8_small.cuh -- the block-scaled FP8 GEMM for few tokens, dense and over experts: the
 // kinds, operands and results of gemm_f8_block.cuh.
 //
+// FB_UP takes slot s's row of token order[s] / k itself, by TMA row gathers; FB_DOWN writes row
+// order[s].
+//
 // Bound: the weights' stream from HBM.  The 128 tensor-memory lanes hold weight rows and the
 // tokens are the MMA's N (BT = 16 or 32), so a tile wastes little on absent tokens.  A
 // pipeline stage is one K-group of 128 weight rows (16 KB) and its tokens; for FB_UP the gate
@@ -27,6 +30,7 @@ namespace apex {
 
 struct FSArgs {
   FBArgs b;
+  const int32_t* order;   // [slots] (experts)
   int S;       // CTAs of a tile's cluster (1: no split; more: one tile per cluster)
   int early;
 };
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
       if constexpr (KIND == FB_UP) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int f = __ldg(args.order + x.row0 + min(4 * lane + i, x.rows - 1));
+          const int f = __ldg(fs.order + x.row0 + min(4 * lane + i, x.rows - 1));
           r[i] = f >= 0 && f < args.slots ? f / args.top_k : 0;
         }
       }
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
         if (tok < BT && tok < x.rows) {
           int r = x.row0 + tok;
           if constexpr (KIND == FB_UP) {
-            const int f = __ldg(args.order + r);
+            const int f = __ldg(fs.order + r);
             r = f >= 0 && f < args.slots ? f / args.top_k : 0;
           }
           sa[i] = args.sa + (size_t)r * args.G;
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
             if (e < count && n < args.N) {
               int r = x.row0 + tb + e;
               if constexpr (KIND == FB_DOWN) {
-                r = __ldg(args.order + r);
+                r = __ldg(fs.order + r);
                 if (r >= args.slots) r = -1;
               }
               const float v = (e & 1) ? acc[0][e / 2].y : acc[0][e / 2].x;

@@ -283,6 +283,22 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, uint3
       : "memory");
 }
 
+// 2-D tiled bulk tensor store shared -> global (elements outside the map are not written), as
+// part of the thread's current bulk group; and the group's end, the wait until its shared
+// memory has been read, and the wait until everything is written.
+__device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Order this thread's generic-proxy shared-memory writes before later async-proxy reads
 // (tensor core operand fetches).
 __device__ __forceinline__ void fence_proxy_async_smem() {
