@@ -593,8 +593,11 @@ apex_status_t apex_block_norm(const void* x, int32_t dtype, int64_t T, int64_t H
   };
   auto by_width = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
+    // CTAs of at most 256 threads, four of which share an SM, once there are two tokens for each
+    // SM (4096 x 8192: 55 us; one chunk a thread, 1024 threads: 66)
     const bool many = T >= 2 * (int64_t)dev_info().sms;
-    if (many && H <= 8192) return run(apex::block_norm_kernel<DT, 4, 256, 3>, 4);
+    if (many && H <= 4096) return run(apex::block_norm_kernel<DT, 2, 256, 4>, 2);
+    if (many && H <= 8192) return run(apex::block_norm_kernel<DT, 4, 256, 4>, 4);
     if (H <= 8192) return run(apex::block_norm_kernel<DT, 1, 1024, 1>, 1);
     if (H <= 16384) return run(apex::block_norm_kernel<DT, 2, 1024, 1>, 2);
     return run(apex::block_norm_kernel<DT, 4, 1024, 1>, 4);
