@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
+      grid_dep_wait();   // (the wait limit counts from here, not from the grids before)
       constexpr uint32_t idesc = idesc_e4m3(C::BM, BN);
       int it = 0;
       bool ok = true;

@@ -61,6 +61,9 @@ struct FSCfg {
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(NS >= 3, "a ring of stages");
   static_assert(SMEM * CTAS_PER_SM <= 226 * 1024, "shared memory budget");
+  // Two CTAs of these kernels fit an SM's tensor memory, and no other kernel here that
+  // allocates some fits beside one in shared memory (171 KB at least): no CTA waits for tensor
+  // memory that a CTA of another cluster holds while it waits for its own.
   static_assert(TMEM_COLS * CTAS_PER_SM <= 512, "tensor memory budget");
 };
 
@@ -239,6 +242,7 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    grid_dep_wait();   // (the wait limit counts from here, not from the grids before)
     constexpr uint32_t idesc = idesc_e4m3(128, BT);
     int it = 0;
     bool ok = true;

@@ -63,6 +63,53 @@ def test_near_middle_test_covers_every_middle():
         assert np.all((((b + shift) & 0xFFFFF) <= 8) & (b >= 0x3A000000)), d
 
 
+def test_scale_by_a_residual_step_is_the_division():
+    # the kernels form a / 448 as q0 = fl(a * fl(1/448)), then q0 + fl(1/448) * (a - 448 q0) in two
+    # fmas; every mantissa (the operations scale with powers of two)
+    a = np.arange(1 << 23, 1 << 24, dtype=np.float64) * 2.0 ** -23
+    k = np.float64(np.float32(1) / np.float32(448))
+    q0 = (a * k).astype(np.float32).astype(np.float64)
+    residual = a - 448.0 * q0                     # exact: at most 34 bits
+    assert np.array_equal(residual.astype(np.float32), residual)
+    s = (residual.astype(np.longdouble) * k + q0).astype(np.float32)
+    assert np.array_equal(s, a.astype(np.float32) / np.float32(448))
+
+
+def test_two_bounds_and_the_middle_settle_every_rounding():
+    # the kernels' rule in numpy: codes of x r (1 - 2^-21) and x r (1 + 2^-21) that agree are the
+    # quotient's; where they do not, t = fl(x r) within 4 ulp of a middle is replaced by the middle
+    # or its neighbour on the side of x - m s, and others round as they are.  r: 1/s and its
+    # neighbours (an approximate reciprocal is within an ulp).
+    rng = np.random.default_rng(4)
+    n = 1 << 19
+    f32 = np.float32
+    x = rng.standard_normal(n).astype(np.float16).astype(f32)
+    amax = np.maximum(np.abs(x), np.abs(rng.standard_normal(n) * 3).astype(np.float16).astype(f32))
+    amax[::4] = np.abs(x[::4]) * rng.integers(1, 9, n // 4)       # quotients 448 / 1..8: ties too
+    mids = ((ob.TABLE[1:] + ob.TABLE[:-1]) / 2).astype(f32)
+    s = ob.scale_of(amax)
+    x[1::4] = (mids[rng.integers(0, 126, n // 4)] * s[1::4]).astype(np.float16).astype(f32)
+    x = np.where(np.abs(x) > amax, amax, x).astype(f32)
+    keep = (s > 2.0 ** -100) & (x != 0)
+    x, s = x[keep], s[keep]
+    exact = ob.encode(x.astype(np.float64) / s.astype(np.float64))
+    for step in (-1, 0, 1):
+        r = (1 / s.astype(np.float64)).astype(f32)
+        r = (r.view(np.int32) + step).view(f32)
+        lo, hi = (ob.encode((x * (r * f32(1 + d))).astype(f32)) for d in (-2.0 ** -21, 2.0 ** -21))
+        agree = lo == hi
+        assert np.array_equal(lo[agree], exact[agree])
+        assert 0.5 < agree.mean() < 1
+        t = (x * r).astype(f32)
+        b = np.abs(t).view(np.int32).astype(np.int64)
+        near = (((b + np.where(b >= 0x3C800000, 0x80004, 4)) & 0xFFFFF) <= 8) & (b >= 0x3A000000)
+        m = np.where(b >= 0x3C800000, (b & 0xFFF00000) | 0x80000, (b + 4) & 0xFFF00000)
+        e = np.abs(x).astype(np.float64) - m.astype(np.int32).view(f32).astype(np.float64) * s
+        m = np.where(near, m + np.sign(e).astype(np.int64), b).astype(np.int32).view(f32)
+        settled = ob.encode(np.copysign(m, t).astype(np.float64))
+        assert np.array_equal(settled, exact)
+
+
 def test_quantizer_oracle_bounds():
     x = np.random.default_rng(1).standard_normal((5, 300))
     codes, s = ob.quantize_rows(x)

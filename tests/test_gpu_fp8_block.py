@@ -178,6 +178,17 @@ def test_gemm(apex, M, N, K, dtype):
     assert np.all(err <= bound), float((err / bound).max())
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 512, 400), (40, 256, 272), (300, 512, 528)])
+def test_gemm_output_aligned_to_its_elements_alone(apex, M, N, K):
+    a, sa, w, sw = operands(np.random.default_rng(12), M, N, K)
+    store = torch.full((M * N + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = store[1:1 + M * N].view(M, N)
+    apex.apex_gemm_fp8_block(M, N, K, *(torch.from_numpy(t).cuda() for t in (a, sa, w, sw)), y)
+    ref, S = ob.gemm(a, sa, w, sw)
+    assert np.all(np.abs(host(y) - ref) <= gemm_bound(ref, S, "bf16", -(-K // 128)))
+    assert store[0] == 7.0 and torch.all(store[1 + M * N:] == 7.0)
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 300, 8192), (90, 700, 4096), (700, 5000, 1024)])
 def test_gemm_repeats_to_the_bit(apex, M, N, K):
     ops = [torch.from_numpy(t).cuda() for t in operands(np.random.default_rng(1), M, N, K)]
@@ -308,6 +319,18 @@ def test_route_special_logits(apex, score):
     for groups, tg in ((1, 1), (5, 2)):
         check_route(apex, z, 6, score=score, groups=groups, topk_groups=tg)
     check_route(apex, z[:6], 6, score=score, mask=np.zeros(6, bool))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score,biased,groups", [("softmax", False, 1), ("sigmoid", True, 8)])
+def test_route_many_tokens(apex, score, biased, groups, dtype):
+    # enough tokens for several a warp, the last run ragged
+    rng = np.random.default_rng(13)
+    T, E = 8195, 64
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    check_route(apex, z, 5, dtype=dtype, score=score, groups=groups, topk_groups=max(1, groups // 2),
+                bias=(0.05 * rng.standard_normal(E)).astype(np.float32) if biased else None,
+                mask=rng.random(T) < 0.9, renormalize=biased)
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (16, 8, 64), (333, 3, 20), (77, 5, 512),
