@@ -266,8 +266,8 @@ apex_status_t check_moe(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
 constexpr int64_t kRoutePlanTokens = 64;
 constexpr int kRoutePlanWarps = 16;
 constexpr int64_t kRouteBatchTokens = 8192;
-// From this many choices on a cluster of 8 CTAs groups them.
-constexpr int64_t kPlanClusterChoices = 16384;
+// Up to this many choices one CTA groups them (32 warps, one batch of ids each).
+constexpr int64_t kPlanCtaChoices = 32 * 32 * apex::kPlanBatch;
 
 apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, int64_t T,
                          int32_t E, int32_t k, int32_t score, const void* bias_f32,
@@ -351,11 +351,11 @@ apex_status_t check_plan(const void* ids, int64_t T, int32_t k, int32_t E, const
 
 apex_status_t plan_launch(const int32_t* ids, int64_t S, int32_t E, int32_t* offsets,
                           int32_t* order, cudaStream_t s) {
-  const unsigned ctas = S >= kPlanClusterChoices ? 8u : 1u;
-  const int warps = 32;
+  // one batch of ids a warp as long as that takes 32 warps of one CTA at most; then a cluster
+  const unsigned ctas = S > kPlanCtaChoices ? (unsigned)apex::kPlanCluster : 1u;
+  const int warps = S <= kPlanCtaChoices / 4 ? 8 : 32;
   static thread_local int attr_dev = -1;
-  if (set_smem(apex::plan_kernel, apex::plan_smem(APEX_MAX_EXPERTS, warps), &attr_dev) !=
-      cudaSuccess)
+  if (set_smem(apex::plan_kernel, apex::plan_smem(APEX_MAX_EXPERTS, 32), &attr_dev) != cudaSuccess)
     return launched(cudaErrorUnknown);
   return launched(launch_pdl_cl(apex::plan_kernel, ctas, 32u * warps,
                                 (size_t)apex::plan_smem(E, warps), s, ctas, ids, (int)S, (int)E,

@@ -15,8 +15,8 @@
 // the time of reading them.  So the choice is made on fp32 values with a bound on their errors
 // for the row.  Where two neighbours in the chosen order (or the last chosen and the best left)
 // are closer than their bounds, the chosen and the next few are compared again in 64 bits, a lane
-// each; where groups on either side of the border are, the whole token is.  The chosen experts'
-// scores are always 64-bit.
+// each; where groups on either side of the border are, the groups are; with NaNs, or more near
+// ties than that, the whole token is.  The chosen experts' scores are always 64-bit.
 //
 // The largest values are taken in turn.  Every lane first sorts its values as 32-bit keys whose
 // low bits are replaced by the register's number, so that a comparator is a maximum and a
@@ -127,45 +127,48 @@ __device__ __forceinline__ double route_sum64(const typename DTraits<DT>::T* z, 
   return sum;
 }
 
+// The groups that stay open, by 64-bit values.
+template <int DT>
+__device__ __noinline__ uint32_t route_open64(const typename DTraits<DT>::T* z, const RouteArgs& a,
+                                              float m, bool poison, double* sv, int lane) {
+  // (without a bias a softmax row's sum divides every group's worth)
+  const double sum = a.bias && !a.sigmoid ? route_sum64<DT>(z, a.E, m, lane) : 1.0;
+#pragma unroll 4
+  for (int e = lane; e < a.E; e += 32) {
+    double w = route_score64(DTraits<DT>::up(z[e]), a.sigmoid, m);
+    if (a.bias) w = (a.sigmoid ? w : sum == 0.0 ? 0.0 : w / sum) + (double)__ldg(a.bias + e);
+    sv[e] = w == w && !poison ? w : ninf_d();   // poison: every score is NaN
+  }
+  __syncwarp();
+  const int lp = lanes_per_group(a.G);
+  const double worth = group_worth<double>(sv, a.E, a.G, lane, lp, ninf_d());
+  __syncwarp();
+  return open_groups(worth, a.G, a.TG, lane, lp);
+}
+
 // The whole choice in 64 bits; returns lane j's j-th expert.
 template <int DT, int EPL>
 __device__ __noinline__ int route_exact(const typename DTraits<DT>::T* z, const RouteArgs& a,
-                                        float m, double* sv, int lane) {
+                                        float m, bool poison, double* sv, int lane) {
   const int E = a.E;
-  const double sum = a.sigmoid ? 1.0 : route_sum64<DT>(z, E, m, lane);
+  const uint32_t open = a.G > 1 ? route_open64<DT>(z, a, m, poison, sv, lane) : 0xffffffffu;
+  const double sum = a.bias && !a.sigmoid ? route_sum64<DT>(z, E, m, lane) : 1.0;
+  const int epg = E / a.G;
   double v[EPL];
   uint32_t left = 0;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 32 * i;
-    double w = ninf_d();
-    if (e < E) {
+    v[i] = ninf_d();
+    if (e < E && (a.G == 1 || ((open >> (e / epg)) & 1u))) {
       left |= 1u << i;
-      w = route_score64(DTraits<DT>::up(z[e]), a.sigmoid, m);
-      if (!a.sigmoid) w = sum == 0.0 ? 0.0 : w / sum;
-      if (a.bias) w += (double)a.bias[e];
-      if (!(w == w)) w = ninf_d();
-      if (a.G > 1) sv[e] = w;
-    }
-#pragma unroll
-    for (int c = 0; c < EPL; ++c) v[c] = c == i ? w : v[c];
-  }
-  if (a.G > 1) {
-    __syncwarp();
-    const int lp = lanes_per_group(a.G);
-    const double worth = group_worth<double>(sv, E, a.G, lane, lp, ninf_d());
-    __syncwarp();
-    const uint32_t open = open_groups(worth, a.G, a.TG, lane, lp);
-    const int epg = E / a.G;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E && !((open >> ((lane + 32 * i) / epg)) & 1u)) left &= ~(1u << i);
-  }
-  if (!a.bias) {   // the order of the logits
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const double w = lane + 32 * i < E ? (double)DTraits<DT>::up(z[lane + 32 * i]) : ninf_d();
-      v[i] = w == w ? w : ninf_d();
+      const float zi = DTraits<DT>::up(z[e]);
+      double w = (double)zi;   // without a bias: the order of the logits
+      if (a.bias) {
+        w = route_score64(zi, a.sigmoid, m);
+        w = (a.sigmoid ? w : sum == 0.0 ? 0.0 : w / sum) + (double)__ldg(a.bias + e);
+      }
+      if (w == w) v[i] = w;
     }
   }
   int mine = -1;
@@ -353,7 +356,8 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
       // (as keys, for one warp-wide minimum and maximum; a NaN decides nothing: 64 bits)
       const uint32_t low = kept ? route_key(worth - err) : 0xffffffffu;
       const uint32_t high = g < a.G && !kept ? route_key(worth + err) : 0u;
-      unsure = __reduce_min_sync(0xffffffffu, low) <= __reduce_max_sync(0xffffffffu, high);
+      if (__reduce_min_sync(0xffffffffu, low) <= __reduce_max_sync(0xffffffffu, high))
+        open = route_open64<DT>(z, a, r.m, r.poison, sv, lane);
     }
   }
   // keys: the value (without a bias: the logit) in the upper bits, NaN as -inf and a closed or
@@ -392,7 +396,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
   };
   if (whole) {
     rounds(0, a.k);
-    if (__any_sync(0xffffffffu, unsure)) r.id = route_exact<DT, EPL>(z, a, r.m, sv, lane);
+    if (__any_sync(0xffffffffu, unsure)) r.id = route_exact<DT, EPL>(z, a, r.m, r.poison, sv, lane);
   } else {
     rounds(0, min(32, a.k + 1));
     if (a.bias == nullptr) F = 0.0f;   // logits are compared as they are
@@ -416,7 +420,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
         r.id = route_candidates<DT>(z, a, r.m, r.id,
                                     __popc(__ballot_sync(0xffffffffu, lane < n && mine != 0u)), lane);
       else
-        r.id = route_exact<DT, EPL>(z, a, r.m, sv, lane);
+        r.id = route_exact<DT, EPL>(z, a, r.m, r.poison, sv, lane);
     }
   }
   return r;
@@ -503,7 +507,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 // writes, with the places of equal ids among 32 from one ballot for each bit of an id (a
 // hardware match takes 60 cycles of a unit that the whole SM shares).  The atomics only count:
 // the result does not depend on the order in which the warps run.
-constexpr int kPlanBatch = 8;   // loads in flight
+constexpr int kPlanBatch = 16;    // loads in flight
+constexpr int kPlanCluster = 8;
 struct PlanShared {
   int* cnt;     // [warps][E]
   int* tot;     // [E] of this CTA (read by the cluster's other CTAs)
@@ -524,25 +529,34 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
   __syncwarp();
   int bits = 0;
   while ((1 << bits) < E + 1) ++bits;
-  for (int i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
-    int id[kPlanBatch];
+  int id[kPlanBatch];   // a run of one batch stays here for the second walk
+  auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < kPlanBatch; ++u) {
       const int i = i0 + 32 * u + lane;
-      id[u] = i < end ? ids[i] : -1;
+      id[u] = i < end ? ids[i] : E;
+      if (id[u] < 0 || id[u] >= E) id[u] = E;   // none
     }
+  };
+  for (int i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
+    load(i0);
 #pragma unroll
     for (int u = 0; u < kPlanBatch; ++u)
-      if (id[u] >= 0 && id[u] < E) atomicAdd(mine + id[u], 1);   // counts alone: any order
+      if (id[u] < E) atomicAdd(mine + id[u], 1);   // counts alone: any order
   }
   __syncthreads();
   // counts -> exclusive sums over this CTA's warps, and the CTA's totals
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int sum = 0;
-    for (int w = 0; w < warps; ++w) {
-      const int c = s.cnt[w * E + e];
-      s.cnt[w * E + e] = sum;
-      sum += c;
+    for (int w0 = 0; w0 < warps; w0 += 8) {   // (warps is a multiple of 8)
+      int c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c[u] = s.cnt[(w0 + u) * E + e];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        s.cnt[(w0 + u) * E + e] = sum;
+        sum += c[u];
+      }
     }
     s.tot[e] = sum;
   }
@@ -557,14 +571,20 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
     const int e = e0 + threadIdx.x;
     int all = 0, before = 0;
     if (e < E) {
-      for (int c = 0; c < ctas; ++c) {
-        int n = s.tot[e];
-        if (ctas > 1) {
+      if (ctas > 1) {
+        int n[kPlanCluster];
+#pragma unroll
+        for (int c = 0; c < kPlanCluster; ++c) {
           const uint32_t remote = cluster_map(smem_u32(s.tot + e), (uint32_t)c);
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(remote) : "memory");
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n[c]) : "r"(remote) : "memory");
         }
-        all += n;
-        if (c < rank) before += n;
+#pragma unroll
+        for (int c = 0; c < kPlanCluster; ++c) {
+          all += n[c];
+          before += c < rank ? n[c] : 0;
+        }
+      } else {
+        all = s.tot[e];
       }
     }
     int v = all;
@@ -575,11 +595,15 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
     }
     if (lane == 31) s.part[warp] = v;
     __syncthreads();
-    int below = carry, whole = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) below += s.part[w];
-      whole += s.part[w];
+    int p = lane < warps ? s.part[lane] : 0;   // every warp: the sums of the warps before it
+    const int mine_w = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += u;
     }
+    const int whole = __shfl_sync(0xffffffffu, p, 31);
+    const int below = carry + __shfl_sync(0xffffffffu, p - mine_w, warp);
     if (e < E) {
       s.base[e] = below + v - all + before;
       if (rank == 0) offsets[e] = below + v - all;
@@ -590,16 +614,12 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
   if (rank == 0 && threadIdx.x == 0) offsets[E] = carry;
   for (int e = lane; e < E; e += 32) mine[e] += s.base[e];
   __syncwarp();
+  const bool again = run > 32 * kPlanBatch;
   for (int i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
-    int id[kPlanBatch];
+    if (again) load(i0);
 #pragma unroll
     for (int u = 0; u < kPlanBatch; ++u) {
-      const int i = i0 + 32 * u + lane;
-      id[u] = i < end ? ids[i] : -1;
-      if (id[u] < 0 || id[u] >= E) id[u] = E;   // none
-    }
-#pragma unroll
-    for (int u = 0; u < kPlanBatch; ++u) {
+      if (i0 + 32 * u >= end) break;
       uint32_t same = 0xffffffffu;   // the lanes with this lane's id
       for (int b = 0; b < bits; ++b) {
         const uint32_t set = __ballot_sync(0xffffffffu, (id[u] >> b) & 1);
