@@ -266,8 +266,12 @@ apex_status_t check_moe(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
 constexpr int64_t kRoutePlanTokens = 64;
 constexpr int kRoutePlanWarps = 16;
 constexpr int64_t kRouteBatchTokens = 8192;
-// Up to this many choices one CTA groups them (32 warps, one batch of ids each).
-constexpr int64_t kPlanCtaChoices = 32 * 32 * apex::kPlanBatch;
+// Grouping: one CTA of 8 warps, a cluster of 8 such, a cluster of 16 CTAs of 16 warps.  With 512
+// choices they take 3.6, 4.1 and 5.1 us; with 1600 5.2, 4.4 and 5.1; with 8000 14.9, 5.7 and 5.7;
+// with 131072 214, 31 and 12.7 (8 CTAs of 16 warps: 20.5).
+constexpr int64_t kPlanCtaChoices = 768;
+constexpr int64_t kPlanClusterChoices = 8192;
+constexpr int kPlanWarps = 16;
 
 apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, int64_t T,
                          int32_t E, int32_t k, int32_t score, const void* bias_f32,
@@ -300,13 +304,13 @@ apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, 
   return APEX_OK;
 }
 
-template <int DT, int EPL>
+template <int DT, int EPL, bool GROUPS>
 apex_status_t route_launch_t(const apex::RouteArgs& a, int32_t* offsets, int32_t* order,
                              cudaStream_t s) {
   if (offsets) {
-    auto kern = apex::route_plan_kernel<DT, EPL>;
+    auto kern = apex::route_plan_kernel<DT, EPL, GROUPS>;
     const int warps = kRoutePlanWarps;
-    const int route = a.G > 1 ? warps * a.E * 8 : 0, plan = apex::plan_smem(a.E, warps);
+    const int route = GROUPS ? warps * a.E * 8 : 0, plan = apex::plan_smem(a.E, warps);
     constexpr int most = kRoutePlanWarps * APEX_MAX_EXPERTS * 8;
     static thread_local int attr_dev = -1;
     if (set_smem(kern, most, &attr_dev) != cudaSuccess) return launched(cudaErrorUnknown);
@@ -319,18 +323,25 @@ apex_status_t route_launch_t(const apex::RouteArgs& a, int32_t* offsets, int32_t
   int64_t blocks = ceil_div(a.T, apex::kRouteWarps * batch);
   const int64_t cap = (int64_t)dev_info().sms * 16;
   if (blocks > cap) blocks = cap;
-  return launched(launch_pdl(apex::route_kernel<DT, EPL>, (unsigned)blocks,
+  return launched(launch_pdl(apex::route_kernel<DT, EPL, GROUPS>, (unsigned)blocks,
                              32 * apex::kRouteWarps,
-                             a.G > 1 ? (size_t)apex::kRouteWarps * a.E * 8 : 0, s, a, batch));
+                             GROUPS ? (size_t)apex::kRouteWarps * a.E * 8 : 0, s, a, batch));
+}
+
+template <int DT, int EPL>
+apex_status_t route_launch_g(const apex::RouteArgs& a, int32_t* offsets, int32_t* order,
+                             cudaStream_t s) {
+  return a.G > 1 ? route_launch_t<DT, EPL, true>(a, offsets, order, s)
+                 : route_launch_t<DT, EPL, false>(a, offsets, order, s);
 }
 
 template <int DT>
 apex_status_t route_launch_e(const apex::RouteArgs& a, int32_t* offsets, int32_t* order,
                              cudaStream_t s) {
-  if (a.E <= 64) return route_launch_t<DT, 2>(a, offsets, order, s);
-  if (a.E <= 128) return route_launch_t<DT, 4>(a, offsets, order, s);
-  if (a.E <= 256) return route_launch_t<DT, 8>(a, offsets, order, s);
-  return route_launch_t<DT, 16>(a, offsets, order, s);
+  if (a.E <= 64) return route_launch_g<DT, 2>(a, offsets, order, s);
+  if (a.E <= 128) return route_launch_g<DT, 4>(a, offsets, order, s);
+  if (a.E <= 256) return route_launch_g<DT, 8>(a, offsets, order, s);
+  return route_launch_g<DT, 16>(a, offsets, order, s);
 }
 
 apex_status_t route_launch(const apex::RouteArgs& a, int32_t dtype, int32_t* offsets,
@@ -349,14 +360,45 @@ apex_status_t check_plan(const void* ids, int64_t T, int32_t k, int32_t E, const
   return APEX_OK;
 }
 
+// Whether clusters of that many CTAs of the grouping kernel can run on the current device (above 8
+// is a kernel's own choice).
+bool plan_cluster_fits(int ctas) {
+  if (cudaFuncSetAttribute(apex::plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(32u * kPlanWarps);
+  cfg.dynamicSmemBytes = (size_t)apex::plan_smem(APEX_MAX_EXPERTS, kPlanWarps);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, apex::plan_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return n > 0;
+}
+
 apex_status_t plan_launch(const int32_t* ids, int64_t S, int32_t E, int32_t* offsets,
                           int32_t* order, cudaStream_t s) {
-  // one batch of ids a warp as long as that takes 32 warps of one CTA at most; then a cluster
-  const unsigned ctas = S > kPlanCtaChoices ? (unsigned)apex::kPlanCluster : 1u;
-  const int warps = S <= kPlanCtaChoices / 4 ? 8 : 32;
   static thread_local int attr_dev = -1;
-  if (set_smem(apex::plan_kernel, apex::plan_smem(APEX_MAX_EXPERTS, 32), &attr_dev) != cudaSuccess)
+  static thread_local bool wide = false;   // clusters of 16 run here (not on every part of a GPU)
+  const int before = attr_dev;
+  if (set_smem(apex::plan_kernel, apex::plan_smem(APEX_MAX_EXPERTS, kPlanWarps), &attr_dev) !=
+      cudaSuccess)
     return launched(cudaErrorUnknown);
+  if (attr_dev != before) wide = plan_cluster_fits(apex::kPlanClusterMax);
+  const unsigned ctas = S <= kPlanCtaChoices                ? 1u
+                        : S <= kPlanClusterChoices || !wide ? 8u
+                                                            : (unsigned)apex::kPlanClusterMax;
+  const int warps = S <= kPlanClusterChoices ? 8 : kPlanWarps;
   return launched(launch_pdl_cl(apex::plan_kernel, ctas, 32u * warps,
                                 (size_t)apex::plan_smem(E, warps), s, ctas, ids, (int)S, (int)E,
                                 offsets, order));

@@ -61,52 +61,67 @@ __device__ __forceinline__ void merge2(F& best, F& second, F b2, F s2) {
   best = best >= b2 ? best : b2;
 }
 
-// Worth of this lane's group, lane / lanes_per, from the values sv[E] in shared memory (lanes of
-// groups past G: -inf).
+// A lane's part in the groups' worths: 1 << shift neighbouring lanes share a group.  Made once a
+// warp: the divisions would be a third of a token's instructions.
+struct RouteGroups {
+  int shift;     // lane >> shift: this lane's group (G and above: none)
+  int mine;
+  int n;         // values of a group a lane reads, at most
+  int start;     // the first of them: groups start at different places, for different banks
+  int at;        // this lane's value 0
+  int left;      // values of the group from there on
+  bool pairs;    // a group has more than one expert
+};
+
+__device__ __forceinline__ RouteGroups route_groups(int E, int G, int lane) {
+  RouteGroups q;
+  q.shift = 5;
+  while (G > 32 >> q.shift) --q.shift;
+  const int epg = E / G, s = lane & ((1 << q.shift) - 1);
+  q.mine = lane >> q.shift;
+  q.n = (epg + (1 << q.shift) - 1) >> q.shift;
+  q.start = q.mine % q.n;
+  q.at = q.mine * epg + s;
+  q.left = q.mine < G ? epg - s : 0;
+  q.pairs = epg > 1;
+  return q;
+}
+
+// Worth of this lane's group from the values sv[E] in shared memory (lanes of no group: -inf).
 template <typename F>
-__device__ __forceinline__ F group_worth(const F* sv, int E, int G, int lane, int lanes_per,
-                                         F ninf) {
-  const int epg = E / G, g = lane / lanes_per, s = lane % lanes_per;
+__device__ __forceinline__ F group_worth(const F* sv, const RouteGroups& q, F ninf) {
   F best = ninf, second = ninf;
-  if (g < G) {
-    const int n = (epg + lanes_per - 1) / lanes_per;
-    // groups start at different places of their round, so that they meet different banks
-    int i = g % n;
-    for (int c = 0; c < n; ++c) {
-      const int at = s + lanes_per * i;
-      if (at < epg) {
-        const F w = sv[g * epg + at];
-        second = w > best ? best : w > second ? w : second;
-        best = w > best ? w : best;
-      }
-      i = i + 1 == n ? 0 : i + 1;
-    }
+  const F* v = sv + q.at;
+  int i = q.start;
+#pragma unroll 4
+  for (int c = 0; c < q.n; ++c) {
+    const int off = i << q.shift;
+    const F w = off < q.left ? v[off] : ninf;
+    second = w > best ? best : w > second ? w : second;
+    best = w > best ? w : best;
+    i = i + 1 == q.n ? 0 : i + 1;
   }
-  for (int o = 1; o < lanes_per; o <<= 1) {
+  for (int o = 1; o < 1 << q.shift; o <<= 1) {
     const F b2 = __shfl_xor_sync(0xffffffffu, best, o);
     const F s2 = __shfl_xor_sync(0xffffffffu, second, o);
     merge2(best, second, b2, s2);
   }
-  return epg > 1 ? best + second : best;
+  return q.pairs ? best + second : best;
 }
 
 // The bit set of the TG groups of largest worth, ties to the lowest.
 template <typename F>
-__device__ __forceinline__ uint32_t open_groups(F worth, int G, int TG, int lane, int lanes_per) {
-  const int mine = lane / lanes_per;
+__device__ __forceinline__ uint32_t open_groups(F worth, int G, int TG, const RouteGroups& q,
+                                                int lane) {
   int rank = 0;
+#pragma unroll 4
   for (int g = 0; g < G; ++g) {
-    const F other = __shfl_sync(0xffffffffu, worth, g * lanes_per);
-    rank += other > worth || (other == worth && g < mine);
+    const F other = __shfl_sync(0xffffffffu, worth, g << q.shift);
+    rank += other > worth || (other == worth && g < q.mine);
   }
-  uint32_t set = mine < G && rank < TG && lane % lanes_per == 0 ? 1u << mine : 0u;
+  const bool first = (lane & ((1 << q.shift) - 1)) == 0;
+  const uint32_t set = q.mine < G && rank < TG && first ? 1u << q.mine : 0u;
   return __reduce_or_sync(0xffffffffu, set);
-}
-
-__device__ __forceinline__ int lanes_per_group(int G) {
-  int p = 32;
-  while (G > 32 / p) p >>= 1;   // 32 / p >= G groups of p lanes
-  return p;
 }
 
 // A logit's score before normalization, in 64 bits.
@@ -140,10 +155,10 @@ __device__ __noinline__ uint32_t route_open64(const typename DTraits<DT>::T* z, 
     sv[e] = w == w && !poison ? w : ninf_d();   // poison: every score is NaN
   }
   __syncwarp();
-  const int lp = lanes_per_group(a.G);
-  const double worth = group_worth<double>(sv, a.E, a.G, lane, lp, ninf_d());
+  const RouteGroups q = route_groups(a.E, a.G, lane);
+  const double worth = group_worth<double>(sv, q, ninf_d());
   __syncwarp();
-  return open_groups(worth, a.G, a.TG, lane, lp);
+  return open_groups(worth, a.G, a.TG, q, lane);
 }
 
 // The whole choice in 64 bits; returns lane j's j-th expert.
@@ -261,9 +276,11 @@ __device__ __forceinline__ void route_load(const RouteArgs& a, long long t, int 
     zv[i] = lane + 32 * i < a.E ? DTraits<DT>::up(z[lane + 32 * i]) : ninf_f();
 }
 
-template <int DT, int EPL>
+template <int DT, int EPL, bool GROUPS>
 __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long long t,
-                                                    const float (&zv)[EPL], double* sv,
+                                                    const float (&zv)[EPL],
+                                                    const RouteGroups& q,
+                                                    const uint32_t (&of)[EPL / 4 + 1], double* sv,
                                                     float bmax, int lane) {
   RouteChoice r;
   r.id = -1;
@@ -273,7 +290,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
   if (a.mask && !a.mask[t]) return r;
   const int E = a.E;
   const typename DTraits<DT>::T* z = static_cast<const typename DTraits<DT>::T*>(a.logits) + t * E;
-  const bool plain = a.bias == nullptr && a.G == 1;
+  const bool plain = a.bias == nullptr && !GROUPS;
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) v[i] = zv[i];
@@ -336,22 +353,20 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     }
   }
   uint32_t open = 0xffffffffu;
-  const int epg = E / a.G;
   bool unsure = false;
-  if (a.G > 1) {
+  if (GROUPS) {
     float* s32 = reinterpret_cast<float*>(sv);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (lane + 32 * i < E) s32[lane + 32 * i] = v[i] == v[i] ? v[i] : ninf_f();
     __syncwarp();
-    const int lp = lanes_per_group(a.G);
-    const float worth = group_worth<float>(s32, E, a.G, lane, lp, ninf_f());
+    const float worth = group_worth<float>(s32, q, ninf_f());
     __syncwarp();
-    open = open_groups(worth, a.G, a.TG, lane, lp);
+    open = open_groups(worth, a.G, a.TG, q, lane);
     if (a.TG < a.G) {
       // two values, each within F, and the rounding of their sum, on either side of the border
       const float err = 2.0f * F + fabsf(worth) * 0x1p-23f;
-      const int g = lane / lp;
+      const int g = q.mine;
       const bool kept = g < a.G && ((open >> g) & 1u);
       // (as keys, for one warp-wide minimum and maximum; a NaN decides nothing: 64 bits)
       const uint32_t low = kept ? route_key(worth - err) : 0xffffffffu;
@@ -370,7 +385,8 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 32 * i;
-    const bool in = e < E && (a.G == 1 || ((open >> (e / epg)) & 1u));
+    const bool in =
+        e < E && (!GROUPS || (__funnelshift_r(open, 0u, of[i / 4] >> (8 * (i % 4))) & 1u));
     const float w = a.bias ? v[i] : zv[i];
     const uint32_t k32 = route_key(w == w ? w : ninf_f());
     const uint32_t low = low_bits - (whole ? (uint32_t)e : (uint32_t)i);
@@ -455,7 +471,7 @@ __device__ __forceinline__ void route_write(const RouteArgs& a, long long t0, in
 }
 
 // Tokens first, first + step, ..., `batch` (32 / kp at most) neighbours at a time.
-template <int DT, int EPL>
+template <int DT, int EPL, bool GROUPS>
 __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first, long long step,
                                              int batch, double* sv, int lane) {
   float bmax = 0.0f;
@@ -464,6 +480,16 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first
   bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
   int kp = 1;
   while (kp < a.k) kp <<= 1;
+  RouteGroups q = {};
+  if (GROUPS) q = route_groups(a.E, a.G, lane);
+  uint32_t of[EPL / 4 + 1];   // the groups of this lane's experts, a byte each
+#pragma unroll
+  for (int i = 0; i < EPL / 4 + 1; ++i) of[i] = 0u;
+  if (GROUPS) {
+    const int epg = a.E / a.G;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) of[i / 4] |= (uint32_t)((lane + 32 * i) / epg) % 32u << (8 * (i % 4));
+  }
   for (long long t0 = first * batch; t0 < a.T; t0 += step * batch) {
     RouteChoice all;
     all.id = -1;
@@ -475,7 +501,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first
     for (int b = 0; b < batch && t0 + b < a.T; ++b) {
       float zn[EPL];   // the next token's logits are on their way meanwhile
       if (b + 1 < batch && t0 + b + 1 < a.T) route_load<DT, EPL>(a, t0 + b + 1, lane, zn);
-      const RouteChoice r = route_choose<DT, EPL>(a, t0 + b, zv, sv, bmax, lane);
+      const RouteChoice r = route_choose<DT, EPL, GROUPS>(a, t0 + b, zv, q, of, sv, bmax, lane);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) zv[i] = zn[i];
       const int id = __shfl_sync(0xffffffffu, r.id, lane & (kp - 1));
@@ -488,15 +514,15 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first
   }
 }
 
-template <int DT, int EPL>
+template <int DT, int EPL, bool GROUPS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a, int batch) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ double s_v[];   // [kRouteWarps][E] with groups
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  route_tokens<DT, EPL>(a, (long long)blockIdx.x * kRouteWarps + warp,
+  route_tokens<DT, EPL, GROUPS>(a, (long long)blockIdx.x * kRouteWarps + warp,
                         (long long)gridDim.x * kRouteWarps, batch,
-                        s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
+                        s_v + (GROUPS ? (size_t)warp * a.E : 0), lane);
 }
 
 // Groups the flat indices i = t * k + j of ids by expert, in ascending order within each:
@@ -508,7 +534,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 // hardware match takes 60 cycles of a unit that the whole SM shares).  The atomics only count:
 // the result does not depend on the order in which the warps run.
 constexpr int kPlanBatch = 16;    // loads in flight
-constexpr int kPlanCluster = 8;
+constexpr int kPlanClusterMax = 16;
 struct PlanShared {
   int* cnt;     // [warps][E]
   int* tot;     // [E] of this CTA (read by the cluster's other CTAs)
@@ -572,14 +598,16 @@ __device__ __forceinline__ void plan_experts_cta(const int32_t* ids, int S, int 
     int all = 0, before = 0;
     if (e < E) {
       if (ctas > 1) {
-        int n[kPlanCluster];
+        int n[kPlanClusterMax];
 #pragma unroll
-        for (int c = 0; c < kPlanCluster; ++c) {
+        for (int c = 0; c < kPlanClusterMax; ++c) {
+          n[c] = 0;
+          if (c >= ctas) continue;
           const uint32_t remote = cluster_map(smem_u32(s.tot + e), (uint32_t)c);
           asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n[c]) : "r"(remote) : "memory");
         }
 #pragma unroll
-        for (int c = 0; c < kPlanCluster; ++c) {
+        for (int c = 0; c < kPlanClusterMax; ++c) {
           all += n[c];
           before += c < rank ? n[c] : 0;
         }
@@ -664,14 +692,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
 }
 
 // Routing and grouping of a few tokens in one CTA: a decode step is bound by its launches.
-template <int DT, int EPL>
+template <int DT, int EPL, bool GROUPS>
 __global__ void __launch_bounds__(512) route_plan_kernel(const RouteArgs a, int32_t* offsets,
                                                          int32_t* order) {
   grid_dep_wait();
   grid_dep_launch();
   extern __shared__ double s_v[];   // [warps][E] with groups; the counting sort's arrays after
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  route_tokens<DT, EPL>(a, warp, warps, 1, s_v + (a.G > 1 ? (size_t)warp * a.E : 0), lane);
+  route_tokens<DT, EPL, GROUPS>(a, warp, warps, 1, s_v + (GROUPS ? (size_t)warp * a.E : 0), lane);
   __syncthreads();   // the ids in global memory are this CTA's own writes
   plan_experts_cta(a.ids, a.T * a.k, a.E, offsets, order,
                    plan_shared(reinterpret_cast<int*>(s_v), a.E, warps), 0, 1);

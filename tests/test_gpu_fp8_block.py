@@ -334,7 +334,8 @@ def test_route_many_tokens(apex, score, biased, groups, dtype):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (16, 8, 64), (333, 3, 20), (77, 5, 512),
-                                   (5000, 4, 100), (16384, 8, 256)])
+                                   (5000, 4, 100), (16384, 8, 256), (96, 8, 512), (97, 8, 512), (1024, 8, 512),
+                                   (1025, 8, 512), (8193, 8, 65), (40000, 16, 512)])
 def test_plan(apex, T, k, E):
     rng = np.random.default_rng(T)
     ids = rng.integers(-1, E, (T, k)).astype(np.int32)
