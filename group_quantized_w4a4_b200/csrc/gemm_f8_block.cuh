@@ -185,11 +185,16 @@ __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restri
   const int chunks = K / 16;
   for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < slots; s += gridDim.x * 8) {
     const int f = __ldg(order + s);
-    if (f < 0 || f >= slots) continue;   // no choice
+    uint4* dst = reinterpret_cast<uint4*>(to_codes + (size_t)s * K);
+    if (f < 0 || f >= slots) {
+      // no choice: zeros, for a tile that ends among such slots (NaNs that memory happened to
+      // hold would take the rounding's rare path there, 20 us of a tile's time)
+      for (int c = lane; c < chunks; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
     const int t = f / top_k;
     if (lane == 0) slot_of[f] = s;
     const uint4* src = reinterpret_cast<const uint4*>(codes + (size_t)t * K);
-    uint4* dst = reinterpret_cast<uint4*>(to_codes + (size_t)s * K);
     for (int c0 = 0; c0 < chunks; c0 += 128) {   // four loads in flight
       uint4 v[4];
 #pragma unroll
