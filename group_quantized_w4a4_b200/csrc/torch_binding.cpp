@@ -7,6 +7,7 @@
 // launch is 3); here the whole call costs little more than its launches.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -87,7 +88,9 @@ struct Tensors {
                             shape_text(t.sizes()));
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+    // (not through the dispatcher, which costs 0.5 us a tensor)
+    return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(at::kCUDA, (c10::DeviceIndex)device),
+                                             std::nullopt));
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 };
