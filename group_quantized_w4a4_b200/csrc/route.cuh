@@ -88,8 +88,9 @@ __device__ __forceinline__ RouteGroups route_groups(int E, int G, int lane) {
 }
 
 // Worth of this lane's group from the values sv[E] in shared memory (lanes of no group: -inf).
+// size: the two values' magnitudes together.
 template <typename F>
-__device__ __forceinline__ F group_worth(const F* sv, const RouteGroups& q, F ninf) {
+__device__ __forceinline__ F group_worth(const F* sv, const RouteGroups& q, F ninf, F& size) {
   F best = ninf, second = ninf;
   const F* v = sv + q.at;
   int i = q.start;
@@ -106,6 +107,7 @@ __device__ __forceinline__ F group_worth(const F* sv, const RouteGroups& q, F ni
     const F s2 = __shfl_xor_sync(0xffffffffu, second, o);
     merge2(best, second, b2, s2);
   }
+  size = q.pairs ? fabs(best) + fabs(second) : fabs(best);
   return q.pairs ? best + second : best;
 }
 
@@ -156,7 +158,8 @@ __device__ __noinline__ uint32_t route_open64(const typename DTraits<DT>::T* z, 
   }
   __syncwarp();
   const RouteGroups q = route_groups(a.E, a.G, lane);
-  const double worth = group_worth<double>(sv, q, ninf_d());
+  double size;
+  const double worth = group_worth<double>(sv, q, ninf_d(), size);
   __syncwarp();
   return open_groups(worth, a.G, a.TG, q, lane);
 }
@@ -281,7 +284,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
                                                     const float (&zv)[EPL],
                                                     const RouteGroups& q,
                                                     const uint32_t (&of)[EPL / 4 + 1], double* sv,
-                                                    float bmax, int lane) {
+                                                    int lane) {
   RouteChoice r;
   r.id = -1;
   r.m = ninf_f();
@@ -294,7 +297,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) v[i] = zv[i];
-  float F = 0.0f;   // bound on the error of every v
+  float F = 0.0f;   // bound on the error of every v before the bias
   if (!a.sigmoid) {
     bool nan = false;
     float m = ninf_f();
@@ -345,7 +348,6 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     for (int i = 0; i < EPL; ++i) v[i] = rcp_approx(1.0f + __expf(-v[i]));
   }
   if (!plain) {
-    F += (1.0f + bmax) * 0x1p-23f;
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
@@ -360,12 +362,14 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     for (int i = 0; i < EPL; ++i)
       if (lane + 32 * i < E) s32[lane + 32 * i] = v[i] == v[i] ? v[i] : ninf_f();
     __syncwarp();
-    const float worth = group_worth<float>(s32, q, ninf_f());
+    float size;
+    const float worth = group_worth<float>(s32, q, ninf_f(), size);
     __syncwarp();
     open = open_groups(worth, a.G, a.TG, q, lane);
     if (a.TG < a.G) {
-      // two values, each within F, and the rounding of their sum, on either side of the border
-      const float err = 2.0f * F + fabsf(worth) * 0x1p-23f;
+      // two values, each within F and the rounding of its sum with the bias, and the rounding of
+      // their sum, on either side of the border; an infinite worth lies beyond every finite one
+      const float err = size < -ninf_f() ? 2.0f * F + size * 0x1p-23f : 0.0f;
       const int g = q.mine;
       const bool kept = g < a.G && ((open >> g) & 1u);
       // (as keys, for one warp-wide minimum and maximum; a NaN decides nothing: 64 bits)
@@ -420,7 +424,8 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     auto decode = [](uint32_t k) {
       return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
     };
-    const float cut = (float)EPL * 0x1p-23f;   // what the keys' low bits hide, relative
+    // what the keys' low bits hide, EPL - 1 units, and the rounding of the sum with the bias
+    const float cut = (float)EPL * 0x1p-23f;
     auto apart = [&](uint32_t hi, uint32_t lo) {
       const float x = decode(hi), y = decode(lo);
       return lo == 0u || x - y > 2.0f * F + cut * (fabsf(x) + fabsf(y)) + 0x1p-120f;
@@ -474,10 +479,6 @@ __device__ __forceinline__ void route_write(const RouteArgs& a, long long t0, in
 template <int DT, int EPL, bool GROUPS>
 __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first, long long step,
                                              int batch, double* sv, int lane) {
-  float bmax = 0.0f;
-  if (a.bias)
-    for (int e = lane; e < a.E; e += 32) bmax = fmaxf(bmax, fabsf(__ldg(a.bias + e)));
-  bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
   int kp = 1;
   while (kp < a.k) kp <<= 1;
   RouteGroups q = {};
@@ -501,7 +502,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first
     for (int b = 0; b < batch && t0 + b < a.T; ++b) {
       float zn[EPL];   // the next token's logits are on their way meanwhile
       if (b + 1 < batch && t0 + b + 1 < a.T) route_load<DT, EPL>(a, t0 + b + 1, lane, zn);
-      const RouteChoice r = route_choose<DT, EPL, GROUPS>(a, t0 + b, zv, q, of, sv, bmax, lane);
+      const RouteChoice r = route_choose<DT, EPL, GROUPS>(a, t0 + b, zv, q, of, sv, lane);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) zv[i] = zn[i];
       const int id = __shfl_sync(0xffffffffu, r.id, lane & (kp - 1));

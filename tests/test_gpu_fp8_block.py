@@ -305,6 +305,20 @@ def test_route_near_ties_through_the_bias(apex):
     check_route(apex, z, 8, score="sigmoid", bias=bias, groups=8, topk_groups=3)
 
 
+@pytest.mark.parametrize("off", [-np.inf, np.finfo(np.float32).min, -1e9])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups", [(64, 1, 1), (64, 8, 3), (160, 8, 2), (96, 32, 9)])
+def test_route_biases_that_shut_experts_out(apex, E, groups, topk_groups, score, off):
+    rng = np.random.default_rng(14)
+    z = rng.standard_normal((200, E)).astype(np.float32)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    bias[rng.random(E) < 0.4] = off      # some groups keep one expert or none
+    bias[: E // groups] = off
+    if groups == 8:
+        bias[-1] = -off                  # and one that is always chosen
+    check_route(apex, z, 6, score=score, bias=bias, groups=groups, topk_groups=topk_groups)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_special_logits(apex, score):
     rng = np.random.default_rng(11)
