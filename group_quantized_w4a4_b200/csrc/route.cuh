@@ -23,6 +23,8 @@
 // minimum; a round is then one warp-wide maximum and a shift in the lane that had it.  (Values
 // that come from 16-bit logits as they are have those bits free: their keys hold the expert's
 // number and decide exactly, ties to the lowest index.)
+// Measured: 16384 tokens x 256 experts, fp32: softmax 18 us, sigmoid with a bias and 8 groups 32
+// us.  Instructions bound it (59 % of the issue slots); the logits take 2.6 us to read.
 #pragma once
 #include <stdint.h>
 
@@ -533,7 +535,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 // by expert, the counts become the places of its first entry of each expert, and a second walk
 // writes, with the places of equal ids among 32 from one ballot for each bit of an id (a
 // hardware match takes 60 cycles of a unit that the whole SM shares).  The atomics only count:
-// the result does not depend on the order in which the warps run.
+// the result does not depend on the order in which the warps run.  Bound: a few dependent steps
+// for few choices (4662: 5.1 us), the ballots for many (131072: 12.7 us).
 constexpr int kPlanBatch = 16;    // loads in flight
 constexpr int kPlanClusterMax = 16;
 struct PlanShared {
@@ -682,7 +685,7 @@ __device__ __forceinline__ PlanShared plan_shared(int* smem, int E, int warps) {
 }
 constexpr int plan_smem(int E, int warps) { return (warps * E + 2 * E + 32) * 4; }
 
-__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ ids, int S, int E,
+__global__ void __launch_bounds__(512) plan_kernel(const int32_t* __restrict__ ids, int S, int E,
                                                     int32_t* __restrict__ offsets,
                                                     int32_t* __restrict__ order) {
   grid_dep_wait();

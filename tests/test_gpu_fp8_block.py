@@ -178,7 +178,8 @@ def test_gemm(apex, M, N, K, dtype):
     assert np.all(err <= bound), float((err / bound).max())
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 512, 400), (40, 256, 272), (300, 512, 528)])
+@pytest.mark.parametrize("M,N,K", [(3, 512, 400), (40, 256, 272), (300, 512, 528),
+                                   (70, 301, 272), (300, 2045, 528), (150, 1406, 400)])
 def test_gemm_output_aligned_to_its_elements_alone(apex, M, N, K):
     a, sa, w, sw = operands(np.random.default_rng(12), M, N, K)
     store = torch.full((M * N + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
