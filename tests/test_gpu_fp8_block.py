@@ -165,7 +165,8 @@ def operands(rng, M, N, K):
     (1, 1, 16), (1, 128, 128), (2, 130, 144), (7, 1000, 272), (16, 256, 512), (17, 384, 1040),
     (31, 129, 2064), (33, 257, 4096), (64, 500, 640), (65, 512, 384), (100, 300, 3200),
     (127, 127, 112), (129, 640, 896), (200, 1111, 528), (257, 520, 1024), (300, 2000, 272),
-    (1030, 769, 400), (1, 8192, 2048), (16, 4096, 8192), (48, 2048, 4096), (128, 4096, 1024)])
+    (1030, 769, 400), (1, 8192, 2048), (16, 4096, 8192), (48, 2048, 4096), (128, 4096, 1024),
+    (1078, 3841, 272), (1078, 3846, 400), (1200, 4096, 528)])   # tiles of 256 columns
 def test_gemm(apex, M, N, K, dtype):
     a, sa, w, sw = operands(np.random.default_rng(M * N + K), M, N, K)
     y = torch.full((M + 1, N), 7.0, dtype=TYPES[dtype], device="cuda")   # a row behind the last
