@@ -39,8 +39,8 @@ bool make_codes3_map(CUtensorMap* map, const void* base, int64_t Z, int64_t rows
   return r == CUDA_SUCCESS;
 }
 
-// 2-D map over outputs [rows][cols] of `size`-byte elements, written in boxes of 32 rows x
-// box_cols columns from shared memory with that many bytes' swizzle.
+// 2-D map over outputs [rows][cols] of `size`-byte elements (codes, 16-bit values or fp32), written
+// in boxes of 32 rows x box_cols columns from shared memory with that many bytes' swizzle.
 bool make_out_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int size,
                   int box_cols) {
   EncodeTiledFn fn = encode_fn();
@@ -49,8 +49,10 @@ bool make_out_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int 
   cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, 32u};
   cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = fn(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-                  base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUtensorMapDataType type = size == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  CUresult r = fn(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   box_cols * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -82,6 +84,8 @@ apex_status_t launch_fb(const void* a_codes, int64_t a_rows, const void* w_codes
     return APEX_ERR_CUDA;
   if (KIND == apex::FB_UP) {
     if (!make_out_map(&my, a.hq, a_rows, a.N, 1, 64)) return APEX_ERR_CUDA;
+  } else if (KIND == apex::FB_DOWN) {
+    if (!make_out_map(&my, a.y, a_rows, a.N, 4, 32)) return APEX_ERR_CUDA;
   } else if (a.y_map) {
     if (!make_out_map(&my, a.y, a_rows, a.N, 2, 64)) return APEX_ERR_CUDA;
   } else {
@@ -244,7 +248,7 @@ MoeWork moe_work(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   w.hq = w.slot + (small ? 0 : pad256(S * 4));
   w.hs = w.hq + pad256(S * I);
   w.y = w.hs + pad256(S * ceil_div(I, 128) * 4);
-  w.total = w.y + pad256(S * H * 2);
+  w.total = w.y + pad256(S * H * 4);
   return w;
 }
 
@@ -578,20 +582,18 @@ apex_status_t apex_moe_mlp_fp8_block(int64_t T, int32_t E, int32_t k, int64_t H,
 
   FBArgs down = with_experts(fb_args(S, H, I, ws + w.hs, w2_scales));
   down.y = ws + w.y;
-  down.y_map = 1;
   const bool f16 = dtype == APEX_DTYPE_F16;
-  st = f16 ? fb_experts<apex::FB_DOWN, apex::DT_F16>(ws + w.hq, S, w2_codes, down, order, s)
-           : fb_experts<apex::FB_DOWN, apex::DT_BF16>(ws + w.hq, S, w2_codes, down, order, s);
+  st = fb_experts<apex::FB_DOWN, apex::DT_F32>(ws + w.hq, S, w2_codes, down, order, s);
   if (st != APEX_OK) return st;
 
   const unsigned blocks = grid_for(T * (H / 8), 256, 16);
   const int32_t* slot_of = small ? nullptr : reinterpret_cast<const int32_t*>(ws + w.slot);
   return launched(f16 ? launch_pdl(apex::combine_kernel<apex::DT_F16>, blocks, 256, 0, s,
-                                   (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
+                                   (const float*)(ws + w.y), static_cast<const float*>(weights_f32),
                                    static_cast<const int32_t*>(ids_i32), slot_of, (int)T, (int)H,
                                    (int)k, (int)E, y)
                       : launch_pdl(apex::combine_kernel<apex::DT_BF16>, blocks, 256, 0, s,
-                                   (const void*)(ws + w.y), static_cast<const float*>(weights_f32),
+                                   (const float*)(ws + w.y), static_cast<const float*>(weights_f32),
                                    static_cast<const int32_t*>(ids_i32), slot_of, (int)T, (int)H,
                                    (int)k, (int)E, y));
 }

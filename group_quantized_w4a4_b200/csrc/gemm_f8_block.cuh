@@ -15,7 +15,9 @@
 //             128 up rows.  The rows are slots: f8_permute_kernel has copied each token's
 //             codes to the slots of its choices (fetching scattered rows here by TMA gathers of
 //             four took 1.5 us a K-group, three times the products).
-//   FB_DOWN   h . W^T of each slot's expert, by slot.
+//   FB_DOWN   h . W^T of each slot's expert, by slot, in fp32: a token's weights multiply its
+//             choices' rows before the one rounding, and a row alone may leave fp16's range or
+//             cancel against another (16-bit rows: inf for 0.1 * 70000, and 1.4 times the error).
 //
 // Tile: 128 tokens (MMA M) x BN weight rows (MMA N), one K-group per pipeline stage, both
 // operands by TMA with 128-byte swizzle; the group's partial goes to one of 512 / BN
@@ -52,7 +54,7 @@ struct FBArgs {
   const int32_t* offsets;   // [E + 1]
   const float* sa;          // [rows][G]
   const float* sw;          // [E (x 2 for FB_UP)][NB][G]
-  void* y;                  // [rows][N]
+  void* y;                  // [rows][N], 16-bit; FB_DOWN: fp32
   uint8_t* hq;              // FB_UP: codes [slots][N] and scales [slots][NB]
   float* hs;
   int s_vec;                // scale rows readable as 16-byte blocks of 4 groups
@@ -503,9 +505,11 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
       // eight K-groups.  Rows of the last, partly filled tile of an expert, which other rows
       // follow, are stored one by one, and so are outputs no map can describe.
       uint8_t* stage = smem + C::OFF_ST + (warp - 4) * C::ST_WARP;
-      if (elect_one()) bulk_wait_read();   // the last tile's
-      __syncwarp();
-      const bool whole = 32 * lq + 32 <= x_rows || KIND == FB_DENSE;
+      if constexpr (KIND != FB_DOWN) {
+        if (elect_one()) bulk_wait_read();   // the last tile's
+        __syncwarp();
+      }
+      const bool whole = 32 * lq + 32 <= x_rows;
       if constexpr (KIND == FB_UP) {
         // h of this thread's 64 columns, the group's maximum with the thread that holds the
         // row's other 64, then the codes
@@ -557,6 +561,45 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
             __syncwarp();
           }
         }
+      } else if constexpr (KIND == FB_DOWN) {
+        // fp32 rows, 32 columns at a time through two buffers in turn: every part, stored by bulk
+        // or not, is one bulk group, so all but the last group read means that its buffer is free
+        if (ok) {
+          const int n0 = x_tn * BN + half * C::CPT;
+          float* y = static_cast<float*>(args.y);
+#pragma unroll
+          for (int b = 0; b < C::CPT / 32; ++b) {
+            uint8_t* buf = stage + (b & 1) * 4096;
+            const int n = n0 + 32 * b;
+            if (elect_one()) bulk_wait_read_but1();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float2 lo = acc[b * 16 + 2 * c], hi = acc[b * 16 + 2 * c + 1];
+              *reinterpret_cast<float4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                  make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+            if (whole) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (elect_one()) {
+                if (n < args.N) tma_store_2d(&tmY, smem_u32(buf), n, x_row0 + 32 * lq);
+                bulk_commit();
+              }
+            } else {   // an expert's last rows: N % 16 == 0, 16-byte rows
+              __syncwarp();
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {   // 4 rows each
+                const int r = i * 4 + (lane >> 3), c = lane & 7;
+                if (32 * lq + r < x_rows && n + 4 * c < args.N)
+                  *reinterpret_cast<float4*>(y + (size_t)(x_row0 + 32 * lq + r) * args.N + n + 4 * c) =
+                      *reinterpret_cast<const float4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+              }
+              if (elect_one()) bulk_commit();
+              __syncwarp();
+            }
+          }
+        }
       } else if (ok) {
 #pragma unroll
         for (int pass = 0; pass < C::CPT / 64; ++pass)
@@ -568,7 +611,7 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
                            D::pack(a[2].x, a[2].y), D::pack(a[3].x, a[3].y));
           }
         const int n0 = x_tn * BN + half * C::CPT;
-        if (whole && args.y_map) {
+        if (args.y_map) {
           fence_proxy_async_smem();
           __syncwarp();
           if (elect_one() && 32 * lq < x_rows) {
@@ -578,7 +621,7 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
                 tma_store_2d(&tmY, smem_u32(stage + pass * 4096), n0 + pass * 64, x_row0 + 32 * lq);
             bulk_commit();
           }
-        } else if (KIND == FB_DENSE) {
+        } else {
           // rows of any alignment: a row's 64 columns at a time, in words of two columns where
           // the row lies on words, else in words of two lanes' columns (330 x 5676 x 1520
           // 10.8 us, 8.7 with 5680 columns and the bulk stores; eight 2-byte stores a lane 16.7)
@@ -603,18 +646,6 @@ __global__ void __launch_bounds__(FBCfg<BN>::THREADS, 1)
                 else if (n + 1 < args.N) dst[1] = (uint16_t)(w >> 16);
               }
             }
-          }
-          __syncwarp();
-        } else {   // an expert's last rows: N % 16 == 0, 16-byte rows
-          __syncwarp();
-#pragma unroll 1
-          for (int i = 0; i < C::CPT / 8; ++i) {   // 4 rows of 64 columns each
-            const int pass = i >> 3, r = (i & 7) * 4 + (lane >> 3), c = lane & 7;
-            const int n = n0 + pass * 64 + c * 8;
-            if (32 * lq + r < x_rows && n < args.N)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.y) +
-                                        (size_t)(x_row0 + 32 * lq + r) * args.N + n) =
-                  *reinterpret_cast<const uint4*>(stage + pass * 4096 + r * 128 + ((c ^ (r & 7)) << 4));
           }
           __syncwarp();
         }

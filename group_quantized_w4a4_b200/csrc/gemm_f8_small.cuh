@@ -2,7 +2,7 @@
 // kinds, operands and results of gemm_f8_block.cuh.
 //
 // FB_UP takes slot s's row of token order[s] / k itself, by TMA row gathers; FB_DOWN writes row
-// order[s].
+// order[s], in fp32.
 //
 // Bound: the weights' stream from HBM.  The 128 tensor-memory lanes hold weight rows and the
 // tokens are the MMA's N (BT = 16 or 32), so a tile wastes little on absent tokens.  A
@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(192, FSCfg<BT, KIND>::CTAS_PER_SM)
                 if (r >= args.slots) r = -1;
               }
               const float v = (e & 1) ? acc[0][e / 2].y : acc[0][e / 2].x;
-              if (r >= 0) static_cast<typename D::T*>(args.y)[(size_t)r * args.N + n] = D::one(v);
+              if (r >= 0) {
+                if constexpr (KIND == FB_DOWN) static_cast<float*>(args.y)[(size_t)r * args.N + n] = v;
+                else static_cast<typename D::T*>(args.y)[(size_t)r * args.N + n] = D::one(v);
+              }
             }
           }
         }

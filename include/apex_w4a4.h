@@ -495,8 +495,8 @@ apex_status_t apex_route_plan_experts(const void *logits, int32_t dtype, int64_t
  * The experts' products: x [T][H] (fp16 / bf16) is quantized (1 x 128 groups), and
  *   h = silu(x . Wg[e]^T) * (x . Wu[e]^T), quantized in groups of 128 from its fp32 values,
  *   y[t] = sum_j weights[t][j] * (h . W2[e]^T), e = ids[t][j], over the ids in [0, E),
- * with each product rounded to x's type before the fp32 sum over j.  A token without experts
- * gets zeros.
+ * with the products and the sum over j in fp32, rounded to x's type once.  A token without
+ * experts gets zeros.
  *   w13 codes [E][2][I][H] (gate, up), scales [E][2][ceil(I/128)][ceil(H/128)];
  *   w2 codes [E][H][I], scales [E][ceil(H/128)][ceil(I/128)]  (apex_pack_weights_fp8_block)
  *   weights, ids: as from apex_route_experts; offsets, order: apex_plan_experts of these ids.
