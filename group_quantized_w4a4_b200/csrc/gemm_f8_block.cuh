@@ -171,8 +171,12 @@ __device__ __forceinline__ float at4(const float4& v, int j) {
   return j < 2 ? (j == 0 ? v.x : v.y) : (j == 2 ? v.z : v.w);
 }
 
+// g * sigmoid(g) * u.  With t = exp(-|g|) <= 1, sigmoid is 1 / (1 + t) or t / (1 + t): nothing
+// overflows, and the divisor in [1, 2] has a reciprocal within an ulp.  (1 / (1 + exp(-g)) by the
+// same reciprocal is 0 below g = -87.3, and the fast exponential's error grows with |g|.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return g * rcp_approx(1.0f + __expf(-g)) * u;
+  const float t = expf(-fabsf(g));
+  return g * ((g < 0.0f ? t : 1.0f) * rcp_approx(1.0f + t)) * u;
 }
 
 // Every token's codes and scales to the slots of its choices: slot s gets row order[s] / k, and
