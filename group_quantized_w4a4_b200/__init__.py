@@ -158,8 +158,27 @@ def load_library(build_if_missing: bool = True):
         lib.apex_debug_trace_next_gemm.restype = None
         lib.apex_debug_gemm_plan.argtypes = [I64, I64, I64, I32, I32, P]
         lib.apex_debug_gemm_plan.restype = st
-        from . import fp8_block as _fb
-        _fb.declare(lib)
+        F = ctypes.c_float
+        for name, args in {
+            "apex_quantize_act_fp8_block": [P, I32, I64, I64, P, P, P],
+            "apex_pack_weights_fp8_block": [P, I32, I64, I64, I64, P, P, P],
+            "apex_gemm_fp8_block": [I64, I64, I64, P, P, P, P, I32, P, P],
+            "apex_linear_fp8_block": [I64, I64, I64, P, I32, P, P, P, P, SZ, P],
+            "apex_route_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P],
+            "apex_route_plan_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P,
+                                        P, P, P],
+            "apex_plan_experts": [P, I64, I32, I32, P, P, P],
+            "apex_moe_mlp_fp8_block": [I64, I32, I32, I64, I64, P, I32, P, P, P, P, P, P, P, P, P,
+                                       P, SZ, P],
+            "apex_block_norm": [P, I32, I64, I64, P, P, P, I64, F, P, F, F, P, P, P, P, P],
+        }.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = st
+        lib.apex_linear_fp8_block_workspace_size.argtypes = [I64, I64, I64]
+        lib.apex_linear_fp8_block_workspace_size.restype = SZ
+        lib.apex_moe_mlp_fp8_block_workspace_size.argtypes = [I64, I32, I32, I64, I64]
+        lib.apex_moe_mlp_fp8_block_workspace_size.restype = SZ
         _lib = lib
         return lib
 

@@ -37,32 +37,6 @@ _DTYPES = {torch.float16: APEX_DTYPE_F16, torch.bfloat16: APEX_DTYPE_BF16,
 _SCORES = {"softmax": APEX_SCORE_SOFTMAX, "sigmoid": APEX_SCORE_SIGMOID}
 
 
-def declare(lib):
-    """ctypes signatures (called once by load_library)."""
-    P, I32, I64, SZ, F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
-                          ctypes.c_float)
-    for name, args in {
-        "apex_quantize_act_fp8_block": [P, I32, I64, I64, P, P, P],
-        "apex_pack_weights_fp8_block": [P, I32, I64, I64, I64, P, P, P],
-        "apex_gemm_fp8_block": [I64, I64, I64, P, P, P, P, I32, P, P],
-        "apex_linear_fp8_block": [I64, I64, I64, P, I32, P, P, P, P, SZ, P],
-        "apex_route_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P],
-        "apex_route_plan_experts": [P, I32, I64, I32, I32, I32, P, I32, I32, I32, F, P, P, P, P,
-                                    P, P],
-        "apex_plan_experts": [P, I64, I32, I32, P, P, P],
-        "apex_moe_mlp_fp8_block": [I64, I32, I32, I64, I64, P, I32, P, P, P, P, P, P, P, P, P, P,
-                                   SZ, P],
-        "apex_block_norm": [P, I32, I64, I64, P, P, P, I64, F, P, F, F, P, P, P, P, P],
-    }.items():
-        fn = getattr(lib, name)
-        fn.argtypes = args
-        fn.restype = ctypes.c_int
-    lib.apex_linear_fp8_block_workspace_size.argtypes = [I64, I64, I64]
-    lib.apex_linear_fp8_block_workspace_size.restype = SZ
-    lib.apex_moe_mlp_fp8_block_workspace_size.argtypes = [I64, I32, I32, I64, I64]
-    lib.apex_moe_mlp_fp8_block_workspace_size.restype = SZ
-
-
 def _lib():
     from . import load_library
     return load_library()

@@ -268,3 +268,17 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         apex.gemm_fp8_block(torch.zeros((4, 256), dtype=torch.uint8), torch.zeros(4, 3),
                             torch.zeros((8, 256), dtype=torch.uint8), torch.zeros(1, 2))
+
+
+def test_the_library_loads_without_torch(lib):
+    # as a program does that calls the C entry points on its own pointers
+    import os
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import group_quantized_w4a4_b200 as apex\n"
+            "lib = apex.load_library(build_if_missing=False)\n"
+            "assert lib.apex_select_weight_group(16, 8192, 8192, 1.0, 1.0) in (128, 8192)\n"
+            "assert lib.apex_linear_fp8_block_workspace_size(4, 8, 272) > 0\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=120)
