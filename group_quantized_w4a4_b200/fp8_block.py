@@ -42,6 +42,13 @@ def _lib():
     return load_library()
 
 
+def _check_stream(stream, tensor):
+    """A stream of another device would leave the call on that device's own current stream, which
+    the caller's waits do not order."""
+    if tensor is not None and stream.device_index != tensor.get_device():
+        raise ValueError("expected a stream of the tensors' device")
+
+
 def _call(name, tensors, args, stream):
     """Launch entry point `name`: `tensors` are the tensor arguments (None where absent), all on
     one device; `args(p)` lists the C arguments but the stream, p the device pointers."""
@@ -119,6 +126,7 @@ def _run(name, stream, *args):
     fn = getattr(_native or _load(), name)
     if stream is None:
         return fn(*args)
+    _check_stream(stream, next((a for a in args if isinstance(a, torch.Tensor)), None))
     with torch.cuda.stream(stream):
         return fn(*args)
 
@@ -207,6 +215,8 @@ def pack_weights_fp8_block(w, stream=None):
     """fp16 / bf16 / fp32 [..., N, K] -> (E4M3 codes uint8 of w's shape, scales fp32
     [..., ceil(N/128), ceil(K/128)])."""
     N, K = w.shape[-2:]
+    if stream is not None:
+        _check_stream(stream, w)
     with torch.cuda.stream(stream):   # None: the current one
         codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
         scales = torch.empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), dtype=torch.float32,

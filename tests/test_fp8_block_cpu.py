@@ -282,3 +282,20 @@ def test_the_library_loads_without_torch(lib):
             "assert lib.apex_linear_fp8_block_workspace_size(4, 8, 272) > 0\n")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=120)
+
+
+@pytest.mark.parametrize("call", [
+    lambda t, s: apex.quantize_act_fp8_block(t(4, 256), stream=s),
+    lambda t, s: apex.pack_weights_fp8_block(t(4, 256), stream=s),
+    lambda t, s: apex.gemm_fp8_block(t(4, 256), t(4, 2), t(8, 256), t(1, 2), stream=s),
+    lambda t, s: apex.linear_fp8_block(t(4, 256), t(8, 256), t(1, 2), stream=s),
+    lambda t, s: apex.route_experts(t(2, 8), 2, stream=s),
+    lambda t, s: apex.plan_experts(t(2, 2), 4, stream=s),
+    lambda t, s: apex.moe_mlp_fp8_block(*(t(2, 2) for _ in range(9)), stream=s),
+    lambda t, s: apex.block_norm(t(4, 256), t(256), stream=s)])
+def test_a_stream_of_another_device_is_refused(call):
+    # (the device is compared before anything else is done with the stream or the tensors)
+    class Elsewhere:
+        device_index = 3
+    with pytest.raises(ValueError, match="a stream of the tensors' device"):
+        call(lambda *shape: torch.zeros(shape), Elsewhere())
