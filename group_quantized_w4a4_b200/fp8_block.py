@@ -226,9 +226,13 @@ def pack_weights_fp8_block(w, stream=None):
     return codes, scales
 
 
-def gemm_fp8_block(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None,
-                   stream=None):
-    """Y = block-scaled FP8 GEMM of quantized operands -> [M, N] of `dtype` (fp16 or bf16)."""
+def gemm_fp8_block(a_codes, a_scales, w_codes, w_scales, dtype=None, out=None, stream=None):
+    """Y = block-scaled FP8 GEMM of quantized operands -> [M, N] of `dtype` (fp16 or bf16; None:
+    out's, or bf16)."""
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    elif out is not None and dtype != out.dtype:
+        raise ValueError(f"dtype: out is {out.dtype}, not {dtype}")
     if dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"dtype: expected fp16 or bf16, got {dtype}")
     return _run("gemm", stream, a_codes, a_scales, w_codes, w_scales, dtype == torch.bfloat16,

@@ -299,3 +299,16 @@ def test_a_stream_of_another_device_is_refused(call):
         device_index = 3
     with pytest.raises(ValueError, match="a stream of the tensors' device"):
         call(lambda *shape: torch.zeros(shape), Elsewhere())
+
+
+def test_gemm_refuses_a_dtype_that_is_not_outs():
+    a, sa, w, sw = (torch.zeros((4, 256), dtype=torch.uint8), torch.zeros(4, 2),
+                    torch.zeros((8, 256), dtype=torch.uint8), torch.zeros(1, 2))
+    for dtype, out in ((torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16)):
+        with pytest.raises(ValueError, match="out is"):
+            apex.gemm_fp8_block(a, sa, w, sw, dtype=dtype, out=torch.zeros((4, 8), dtype=out))
+    with pytest.raises(ValueError, match="expected fp16 or bf16"):
+        apex.gemm_fp8_block(a, sa, w, sw, out=torch.zeros((4, 8)))
+    for out in (torch.float16, torch.bfloat16):      # alone, out says the type: no complaint of it
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            apex.gemm_fp8_block(a, sa, w, sw, out=torch.zeros((4, 8), dtype=out))
