@@ -1,5 +1,6 @@
 """Build the CUDA library (sm_100a) in-tree: group_quantized_w4a4_b200/_lib/libapex_w4a4.so,
-and the torch side of its newer calls, _lib/apex_torch.so (plain C++ against torch's headers).
+and the torch side of its newer calls, _lib/apex_torch-<versions of torch and Python>.so (plain
+C++ against torch's headers, whose ABI changes with both).
 
     python -m group_quantized_w4a4_b200.build [--force]
 
@@ -21,7 +22,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libapex_w4a4.so")
-TORCH_LIB_PATH = os.path.join(LIB_DIR, "apex_torch.so")
 TORCH_SRC = os.path.join(CSRC, "torch_binding.cpp")
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -61,24 +61,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def torch_lib_path() -> str:
+    """The torch binding's file: a name for each torch and Python, so that none loads another's."""
+    import torch
+    version = "".join(c if c.isalnum() or c == "." else "_" for c in torch.__version__)
+    return os.path.join(LIB_DIR, f"apex_torch-{version}-{sys.implementation.cache_tag}.so")
+
+
 def torch_is_stale() -> bool:
-    if not os.path.exists(TORCH_LIB_PATH):
+    path = torch_lib_path()
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(TORCH_LIB_PATH)
+    t = os.path.getmtime(path)
     headers = glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(s) > t for s in [TORCH_SRC, *headers])
 
 
 def build_torch(force: bool = False) -> str:
-    """Compile the torch binding if it is older than its sources (or `force`); return its path."""
+    """Compile the torch binding if there is none for this torch and Python, or it is older than its
+    sources (or `force`); return its path."""
+    path = torch_lib_path()
     if not force and not torch_is_stale():
-        return TORCH_LIB_PATH
+        return path
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     include = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cxx = shutil.which("g++") or "g++"
@@ -87,8 +97,8 @@ def build_torch(force: bool = False) -> str:
                     *(f for i in include for f in ("-isystem", i)), TORCH_SRC, "-o", tmp,
                     f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
                     "-lc10", "-lc10_cuda"], check=True)
-    os.replace(tmp, TORCH_LIB_PATH)
-    return TORCH_LIB_PATH
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

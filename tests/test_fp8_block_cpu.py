@@ -312,3 +312,10 @@ def test_gemm_refuses_a_dtype_that_is_not_outs():
     for out in (torch.float16, torch.bfloat16):      # alone, out says the type: no complaint of it
         with pytest.raises(ValueError, match="CUDA tensor"):
             apex.gemm_fp8_block(a, sa, w, sw, out=torch.zeros((4, 8), dtype=out))
+
+
+def test_the_torch_binding_is_of_this_torch(lib, monkeypatch):
+    apex_build.build_torch()
+    assert not apex_build.torch_is_stale()
+    monkeypatch.setattr(torch, "__version__", "9.9.0+other")
+    assert apex_build.torch_is_stale()       # another torch: built again, under another name
