@@ -100,8 +100,8 @@ __device__ __forceinline__ float rcp_approx(float x) {   // within 1 ulp
 __device__ __forceinline__ F8Scale f8_scale(uint32_t amax_bits) {
   const float a = __uint_as_float(amax_bits);
   F8Scale q;
-  // a / 448: the product with the rounded 1/448 is within an ulp, and one residual step (exact
-  // in an fma) makes it the correctly rounded quotient
+  // a / 448 by Markstein's correction: the product with the rounded 1/448 is within an ulp, and one
+  // residual step (exact in an fma) makes it the correctly rounded quotient
   const float k = 1.0f / 448.0f;
   const float q0 = __fmul_rn(a, k);
   q.s = __fmaf_rn(__fmaf_rn(-q0, 448.0f, a), k, q0);

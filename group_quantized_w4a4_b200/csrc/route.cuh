@@ -16,7 +16,9 @@
 // for the row.  Where two neighbours in the chosen order (or the last chosen and the best left)
 // are closer than their bounds, the chosen and the next few are compared again in 64 bits, a lane
 // each; where groups on either side of the border are, the groups are; with NaNs, or more near
-// ties than that, the whole token is.  The chosen experts' scores are always 64-bit.
+// ties than that, the whole token is.  The chosen experts' scores are 64-bit.  What divides them in a
+// softmax without renormalization is a 64-bit sum of fp32 exponentials, each within 1.5 ulp: such
+// weights are within 2^-22 of the exact ones with their rounding, others within 2^-24.
 //
 // The largest values are taken in turn.  Every lane first sorts its values as 32-bit keys whose
 // low bits are replaced by the register's number, so that a comparator is a maximum and a
@@ -251,7 +253,7 @@ struct RouteChoice {
   bool poison;    // softmax: a NaN or +inf logit makes every score NaN
 };
 
-// Sorts EPL keys in descending order (odd-even merge sort network; EPL a power of two).
+// Sorts EPL keys in descending order (Batcher's odd-even merge sort network; EPL a power of two).
 template <int EPL>
 __device__ __forceinline__ void sort_keys(uint32_t (&k)[EPL]) {
 #pragma unroll
@@ -397,7 +399,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     const uint32_t k32 = route_key(w == w ? w : ninf_f());
     const uint32_t low = low_bits - (whole ? (uint32_t)e : (uint32_t)i);
     key[i] = in ? (k32 & ~low_bits) | low : 0u;
-    unsure |= !whole && !(w == w);   // NaNs tie with -inf
+    unsure |= !(w == w);   // NaNs tie with -inf (whole keys tell them apart as 64 bits would)
   }
   sort_keys<EPL>(key);
   uint32_t mine = 0;   // lane j: the j-th largest key
@@ -418,7 +420,6 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
   };
   if (whole) {
     rounds(0, a.k);
-    if (__any_sync(0xffffffffu, unsure)) r.id = route_exact<DT, EPL>(z, a, r.m, r.poison, sv, lane);
   } else {
     rounds(0, min(32, a.k + 1));
     if (a.bias == nullptr) F = 0.0f;   // logits are compared as they are
@@ -450,7 +451,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
 }
 
 // The weights of up to 32 / kp tokens at once, kp lanes each: lane b * kp + j has the j-th choice
-// of token t0 + b.  Scores in 64 bits, one rounding.
+// of token t0 + b.  Scores in 64 bits (but for a softmax's whole sum), one rounding.
 template <int DT>
 __device__ __forceinline__ void route_write(const RouteArgs& a, long long t0, int batch, int kp,
                                             const RouteChoice& r, int lane) {
