@@ -284,6 +284,8 @@ apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, 
   if (!logits || !weights_f32 || !ids_i32 || T <= 0 || E <= 0 || k <= 0 || groups <= 0 ||
       topk_groups <= 0 || topk_groups > groups || E % groups)
     return APEX_ERR_INVALID_ARG;
+  const bool group_max = (score & APEX_GROUP_MAX) != 0;
+  score &= ~APEX_GROUP_MAX;
   if (score != APEX_SCORE_SOFTMAX && score != APEX_SCORE_SIGMOID) return APEX_ERR_INVALID_ARG;
   if (k > topk_groups * (E / groups)) return APEX_ERR_INVALID_ARG;
   if (!is_float(dtype) || E > APEX_MAX_EXPERTS || k > APEX_MAX_TOP_K || groups > 32 ||
@@ -302,6 +304,7 @@ apex_status_t route_args(apex::RouteArgs* a, const void* logits, int32_t dtype, 
   a->TG = topk_groups;
   a->sigmoid = score == APEX_SCORE_SIGMOID;
   a->renorm = renormalize != 0;
+  a->group_max = group_max;
   a->scale = scale;
   a->ids = static_cast<int32_t*>(ids_i32);
   a->weights = static_cast<float*>(weights_f32);

@@ -4,11 +4,11 @@
 //   p = softmax(z) or 1 / (1 + exp(-z))                       (scores)
 //   v = p + bias                                              (values that are compared)
 //   groups > 1: a group of E / groups neighbouring experts is worth the sum of its two largest
-//   v; experts of the topk_groups best groups stay in the choice
+//   v, or its largest alone; experts of the topk_groups best groups stay in the choice
 //   ids = the k largest v, ties to the lowest index;  weights = scale * p[ids], divided by
 //   their sum first when renormalized.
 // The choice is that of v in 64 bits; without a bias the order of v is the order of z, which is
-// compared itself.  A NaN is chosen last; a softmax row of -inf alone has scores 0; weights
+// compared itself (by groups' largest too, so that nothing is left to decide there).  A NaN is chosen last; a softmax row of -inf alone has scores 0; weights
 // whose sum is 0 stay 0.
 //
 // 64-bit exponentials of every logit cost 230 us for 16384 tokens x 256 experts, sixty times
@@ -41,6 +41,7 @@ struct RouteArgs {
   const uint8_t* mask;     // [T] or null: 0 = the token takes no part
   int T, E, k, G, TG;
   int sigmoid, renorm;
+  int group_max;           // a group is worth its largest value alone
   float scale;
   int32_t* ids;            // [T][k]
   float* weights;          // [T][k]
@@ -74,20 +75,21 @@ struct RouteGroups {
   int start;     // the first of them: groups start at different places, for different banks
   int at;        // this lane's value 0
   int left;      // values of the group from there on
-  bool pairs;    // a group has more than one expert
+  bool pairs;    // a group is worth the sum of two experts' values
 };
 
-__device__ __forceinline__ RouteGroups route_groups(int E, int G, int lane) {
+__device__ __forceinline__ RouteGroups route_groups(const RouteArgs& a, int lane) {
   RouteGroups q;
+  const int G = a.G;
   q.shift = 5;
   while (G > 32 >> q.shift) --q.shift;
-  const int epg = E / G, s = lane & ((1 << q.shift) - 1);
+  const int epg = a.E / G, s = lane & ((1 << q.shift) - 1);
   q.mine = lane >> q.shift;
   q.n = (epg + (1 << q.shift) - 1) >> q.shift;
   q.start = q.mine % q.n;
   q.at = q.mine * epg + s;
   q.left = q.mine < G ? epg - s : 0;
-  q.pairs = epg > 1;
+  q.pairs = epg > 1 && !a.group_max;
   return q;
 }
 
@@ -148,6 +150,12 @@ __device__ __forceinline__ double route_sum64(const typename DTraits<DT>::T* z, 
   return sum;
 }
 
+// Whether values are compared as logits: their order is that of the scores, and no sum of two
+// scores is asked for.
+__device__ __forceinline__ bool route_by_logits(const RouteArgs& a) {
+  return a.bias == nullptr && (a.G == 1 || a.group_max);
+}
+
 // The groups that stay open, by 64-bit values.
 template <int DT>
 __device__ __noinline__ uint32_t route_open64(const typename DTraits<DT>::T* z, const RouteArgs& a,
@@ -156,12 +164,13 @@ __device__ __noinline__ uint32_t route_open64(const typename DTraits<DT>::T* z, 
   const double sum = a.bias && !a.sigmoid ? route_sum64<DT>(z, a.E, m, lane) : 1.0;
 #pragma unroll 4
   for (int e = lane; e < a.E; e += 32) {
-    double w = route_score64(DTraits<DT>::up(z[e]), a.sigmoid, m);
+    const float ze = DTraits<DT>::up(z[e]);
+    double w = route_by_logits(a) ? (double)ze : route_score64(ze, a.sigmoid, m);
     if (a.bias) w = (a.sigmoid ? w : sum == 0.0 ? 0.0 : w / sum) + (double)__ldg(a.bias + e);
     sv[e] = w == w && !poison ? w : ninf_d();   // poison: every score is NaN
   }
   __syncwarp();
-  const RouteGroups q = route_groups(a.E, a.G, lane);
+  const RouteGroups q = route_groups(a, lane);
   double size;
   const double worth = group_worth<double>(sv, q, ninf_d(), size);
   __syncwarp();
@@ -297,7 +306,7 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
   if (a.mask && !a.mask[t]) return r;
   const int E = a.E;
   const typename DTraits<DT>::T* z = static_cast<const typename DTraits<DT>::T*>(a.logits) + t * E;
-  const bool plain = a.bias == nullptr && !GROUPS;
+  const bool plain = a.bias == nullptr && (!GROUPS || a.group_max);   // (route_by_logits)
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) v[i] = zv[i];
@@ -364,13 +373,14 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteArgs& a, long lon
     float* s32 = reinterpret_cast<float*>(sv);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (lane + 32 * i < E) s32[lane + 32 * i] = v[i] == v[i] ? v[i] : ninf_f();
+      if (lane + 32 * i < E)
+        s32[lane + 32 * i] = v[i] == v[i] && !(plain && r.poison) ? v[i] : ninf_f();
     __syncwarp();
     float size;
     const float worth = group_worth<float>(s32, q, ninf_f(), size);
     __syncwarp();
     open = open_groups(worth, a.G, a.TG, q, lane);
-    if (a.TG < a.G) {
+    if (a.TG < a.G && !plain) {
       // two values, each within F and the rounding of its sum with the bias, and the rounding of
       // their sum, on either side of the border; an infinite worth lies beyond every finite one
       const float err = size < -ninf_f() ? 2.0f * F + size * 0x1p-23f : 0.0f;
@@ -485,7 +495,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, long long first
   int kp = 1;
   while (kp < a.k) kp <<= 1;
   RouteGroups q = {};
-  if (GROUPS) q = route_groups(a.E, a.G, lane);
+  if (GROUPS) q = route_groups(a, lane);
   uint32_t of[EPL / 4 + 1];   // the groups of this lane's experts, a byte each
 #pragma unroll
   for (int i = 0; i < EPL / 4 + 1; ++i) of[i] = 0u;

@@ -17,6 +17,7 @@ APEX_DTYPE_BF16 = 1
 APEX_DTYPE_F32 = 2
 APEX_SCORE_SOFTMAX = 0
 APEX_SCORE_SIGMOID = 1
+APEX_GROUP_MAX = 0x100
 APEX_MAX_EXPERTS = 512
 APEX_MAX_TOP_K = 32
 
@@ -34,6 +35,7 @@ __all__ = ENTRY_POINTS + CONVENIENCES
 
 _DTYPES = {torch.float16: APEX_DTYPE_F16, torch.bfloat16: APEX_DTYPE_BF16,
            torch.float32: APEX_DTYPE_F32}
+_GROUP_SCORES = {"top2": 0, "max": APEX_GROUP_MAX}
 _SCORES = {"softmax": APEX_SCORE_SOFTMAX, "sigmoid": APEX_SCORE_SIGMOID}
 
 
@@ -245,13 +247,17 @@ def linear_fp8_block(x, w_codes, w_scales, out=None, stream=None):
 
 
 def route_experts(logits, k, bias=None, score="softmax", groups=1, topk_groups=1,
-                  renormalize=True, scale=1.0, mask=None, plan=False, stream=None):
+                  renormalize=True, scale=1.0, mask=None, plan=False, stream=None,
+                  group_score="top2"):
     """logits [T, E] -> (weights fp32 [T, k], ids int32 [T, k]); with plan also (offsets, order)
-    of plan_experts.  bias fp32 [E]; mask bool [T] (False: the token takes no part)."""
+    of plan_experts.  bias fp32 [E]; mask bool [T] (False: the token takes no part).  group_score:
+    a group is worth the sum of its two largest values ("top2") or its largest ("max")."""
     if score not in _SCORES:
         raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
-    return _run("route", stream, logits, k, bias, _SCORES[score], groups, topk_groups,
-                renormalize, scale, mask, plan)
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score: expected one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    return _run("route", stream, logits, k, bias, _SCORES[score] | _GROUP_SCORES[group_score],
+                groups, topk_groups, renormalize, scale, mask, plan)
 
 
 def plan_experts(ids, experts, stream=None):

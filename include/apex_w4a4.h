@@ -454,12 +454,14 @@ apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void 
  * ---- Experts.  Routing: for every token t with logits z[E] (fp16 / bf16 / fp32),
  *   p = softmax(z) or 1 / (1 + exp(-z));  v = p + bias (bias may be NULL)
  *   groups > 1: of the groups of E/groups neighbouring experts, the topk_groups with the
- *     largest sum of their two largest v (one, where a group has one) stay in the choice
+ *     largest sum of their two largest v (one, where a group has one) stay in the choice, as
+ *     routers with a balance bias have it; with APEX_GROUP_MAX added to score, those with the
+ *     largest v, as softmax routers without one do
  *   ids [T][k] = the k largest v in descending order, ties to the lowest index
  *   weights [T][k] = scale * p[ids] (divided by their sum first with renormalize)
  * The choice is that of the exact scores: values are compared in 64 bits (without a bias the
- * logits themselves, whose order is the same; a group's sum is that of its scores).  mask [T] bytes (NULL: all ones): a token with 0
- * gets ids -1 and weights 0.  NaN logits are chosen last and make weights NaN; a softmax row of
+ * logits themselves, whose order is the same; a group's sum is that of its scores).  mask [T]
+ * bytes (NULL: all ones): a token with 0 gets ids -1 and weights 0.  NaN logits are chosen last and make weights NaN; a softmax row of
  * -inf alone has scores 0, and weights that sum to 0 stay 0.
  * E % groups == 0, k <= topk_groups * E / groups, E <= APEX_MAX_EXPERTS, k <= APEX_MAX_TOP_K,
  * groups <= 32.
@@ -468,6 +470,7 @@ apex_status_t apex_linear_fp8_block(int64_t M, int64_t N, int64_t K, const void 
 #define APEX_MAX_TOP_K 32
 #define APEX_SCORE_SOFTMAX 0
 #define APEX_SCORE_SIGMOID 1
+#define APEX_GROUP_MAX 0x100   /* added to the score */
 apex_status_t apex_route_experts(const void *logits, int32_t dtype, int64_t T, int32_t E,
                                  int32_t k, int32_t score, const void *bias_f32, int32_t groups,
                                  int32_t topk_groups, int32_t renormalize, float scale,

@@ -91,7 +91,7 @@ def gemm(a_codes, a_scales, w_codes, w_scales):
 
 
 def route(z, k, bias=None, score="softmax", groups=1, topk_groups=1, renormalize=True, scale=1.0,
-          mask=None):
+          mask=None, group_score="top2"):
     """(weights, ids, scores) by a plain loop over the tokens."""
     T, E = z.shape
     weights, ids, scores = np.zeros((T, k)), np.full((T, k), -1, np.int32), np.zeros((T, E))
@@ -115,7 +115,11 @@ def route(z, k, bias=None, score="softmax", groups=1, topk_groups=1, renormalize
         open_ = list(range(E))
         if groups > 1:
             n = E // groups
-            worth = [sum(sorted(v[g * n:(g + 1) * n])[-2:]) for g in range(groups)]
+            if group_score == "top2":
+                worth = [sum(sorted(v[g * n:(g + 1) * n])[-2:]) for g in range(groups)]
+            else:   # without a bias: by the logits, whose order the scores have
+                u = v if bias is not None else np.where(np.isnan(p), -np.inf, row)
+                worth = [max(u[g * n:(g + 1) * n]) for g in range(groups)]
             kept = sorted(range(groups), key=lambda g: (-worth[g], g))[:topk_groups]
             open_ = [e for e in open_ if e // n in kept]
         if bias is None:      # the order of the scores is that of the logits

@@ -319,3 +319,20 @@ def test_the_torch_binding_is_of_this_torch(lib, monkeypatch):
     assert not apex_build.torch_is_stale()
     monkeypatch.setattr(torch, "__version__", "9.9.0+other")
     assert apex_build.torch_is_stale()       # another torch: built again, under another name
+
+
+def test_route_oracles_two_group_rules():
+    # groups {0,1} {2,3} {4,5}: the largest single score is in the last, the largest pair in the first
+    z = np.array([[1.0, 0.9, 0.5, 0.4, 1.1, -9.0]])
+    assert ob.route(z, 2, groups=3, topk_groups=1)[1].tolist() == [[0, 1]]
+    assert ob.route(z, 2, groups=3, topk_groups=1, group_score="max")[1].tolist() == [[4, 5]]
+    bias = np.array([0, 0, 0, 0.7, 0, 0])      # and by the biased score of the middle's best
+    assert ob.route(z, 2, bias=bias, groups=3, topk_groups=1, group_score="max")[1].tolist() == [[3, 2]]
+
+
+def test_group_rule_refusals(lib):
+    with pytest.raises(ValueError, match="group_score"):
+        apex.route_experts(torch.zeros(2, 8), 2, group_score="mean")
+    for score, code in ((0x200, INVALID), (0x102, INVALID), (0x100, ALIGN), (0x101, ALIGN)):
+        assert lib.apex_route_experts(P(0x1002), 2, 4, 8, 2, score, None, 4, 2, 1, 1.0, None,
+                                      P(0x2000), P(0x3000), None) == code

@@ -646,3 +646,44 @@ def test_gpu_refusals(apex):
     assert e.value.code == apex.APEX_ERR_ALIGNMENT
     with pytest.raises(ValueError):
         apex.linear_fp8_block(x, torch.zeros((8, 256), dtype=torch.uint8), torch.zeros(1, 2))
+
+
+# ------------------------------------------------------------------ groups by their best expert
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,topk_groups", [
+    (1, 160, 6, 8, 3), (777, 160, 6, 8, 3), (64, 256, 8, 8, 4), (9, 96, 2, 3, 1), (21, 8, 3, 8, 4),
+    (37, 512, 32, 32, 16), (50, 64, 4, 4, 4), (8200, 64, 6, 8, 2)])
+def test_route_groups_by_their_best(apex, T, E, k, groups, topk_groups, score):
+    rng = np.random.default_rng(T + E)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    for dtype in ("fp32", "bf16", "fp16"):
+        for bias in (None, (0.1 * rng.standard_normal(E)).astype(np.float32)):
+            check_route(apex, z, k, dtype=dtype, bias=bias, score=score, groups=groups,
+                        topk_groups=topk_groups, renormalize=bias is not None, scale=2.5,
+                        mask=rng.random(T) < 0.7 if dtype == "fp16" else None, group_score="max")
+    if 1 < topk_groups < groups < E and T > 40:    # the two rules are two
+        both = [apex.route_experts(torch.from_numpy(z).cuda(), k, score=score, groups=groups,
+                                   topk_groups=topk_groups, group_score=g)[1] for g in ("top2", "max")]
+        assert not torch.equal(*both)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_by_their_best_at_ties_and_special_logits(apex, score):
+    rng = np.random.default_rng(15)
+    z = rng.integers(-2, 3, (200, 64)).astype(np.float32)    # nearly every value is tied
+    z[0] = 0
+    z[1] = -np.inf
+    z[2, 3:] = -np.inf
+    z[3] = np.finfo(np.float32).min
+    z[4, 5] = np.nan
+    z[5] = np.nan
+    z[6, ::2] = -1e30
+    z[7, :8] = np.nan                    # a whole group
+    for bias in (None, np.zeros(64, np.float32), np.tile(np.float32([0, 0.25]), 32)):
+        check_route(apex, z, 8, score=score, groups=8, topk_groups=3, bias=bias, group_score="max")
+    base = rng.normal(0, 1, (300, 1)).astype(np.float32)      # logits an fp32 ulp apart
+    steps = rng.permuted(np.tile(np.arange(48), (300, 1)), axis=1)
+    z = (base.view(np.int32) + steps).astype(np.int32).view(np.float32)
+    check_route(apex, z, 6, score=score, groups=4, topk_groups=2, group_score="max")
