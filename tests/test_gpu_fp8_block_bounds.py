@@ -193,3 +193,104 @@ def test_moe_silu_of_large_negative_gates(apex, gate, T):
             ids, *apex.plan_experts(ids, 1), c13, s13, ones(1, H, I), torch.ones((1, 1, 1), device="cuda")]
     ref, _ = assert_within(apex, args, "bf16")
     assert np.all((ref < -8) & (ref > -32))
+
+
+@pytest.mark.parametrize("T,E,k,H,I,rows", [
+    (24, 160, 8, 4096, 1536, [0, 23]), (600, 160, 8, 4096, 1536, [5, 599]),
+    (40, 8, 2, 7168, 2048, [0, 7, 39]), (100, 8, 2, 7168, 2048, [3, 99]),
+    (3, 512, 32, 1024, 256, None), (400, 512, 32, 1024, 256, [0, 399]),
+    (4000, 4, 2, 528, 528, [0, 1, 2000, 3998, 3999])])   # several tiles for every SM
+def test_moe_experts_of_large_models(apex, T, E, k, H, I, rows):
+    args = experts_case(apex, 4, T, E, k, H, I, "bf16", choices(T, T, E, k))
+    assert_within(apex, args, "bf16", rows and np.array(rows))
+
+
+# at most 10 rows an expert take one kernel, more the other
+@pytest.mark.parametrize("T", [15, 70])
+def test_moe_bad_tokens_stay_theirs_in_both_kernels(apex, T):
+    ids = choices(T, T, 4, 2)
+    args = experts_case(apex, 5, T, 4, 2, 256, 144, "bf16", ids)
+    args[0][5, 3] = float("nan")
+    args[0][9, 200] = float("inf")
+    y = host(apex.moe_mlp_fp8_block(*args))
+    assert np.isnan(y[5]).all() and not np.isfinite(y[9]).any()
+    keep = [t for t in range(T) if t not in (5, 9)]
+    assert np.isfinite(y[keep]).all()
+
+
+@pytest.mark.parametrize("T", [15, 70])
+def test_moe_offsets_that_do_not_ascend_stay_in_bounds_in_both_kernels(apex, T):
+    # nothing is promised of the values; the kernels clamp what they index with
+    S = 2 * T
+    args = experts_case(apex, 6, T, 4, 2, 144, 80, "bf16", np.zeros((T, 2), np.int32))
+    for bad in ([0, 1 << 30, 3, S, S], [S, 0, S, 0, S], [-5, -4, 7, S + 50, S + 60]):
+        a = list(args)
+        a[3] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        a[4] = torch.randint(-(1 << 31), (1 << 31) - 1, (S,), device="cuda").int()
+        apex.moe_mlp_fp8_block(*a)
+        torch.cuda.synchronize()
+    assert_within(apex, args, "bf16")      # and the same buffers serve a right call
+
+
+# 256-column tiles, three rounds of them over the SMs
+@pytest.mark.parametrize("N", [8192, 8186])
+def test_gemm_several_tiles_for_every_sm(apex, N):
+    M, K = 1300, 2064
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(N)
+    a, _ = random_codes(gen, (M, K), 1.0)
+    w, sw = random_codes(gen, (N, K), 0.01)
+    sa = torch.rand((M, -(-K // 128)), generator=gen, device="cuda") + 0.5
+    y = torch.full((M + 1, N), 7.0, dtype=torch.float16, device="cuda")
+    apex.apex_gemm_fp8_block(M, N, K, a, sa, w, sw, y)
+    n = lambda t: t.cpu().numpy()    # noqa: E731
+    ref, S = ob.gemm(n(a), n(sa), n(w), n(sw))
+    got = host(y)
+    assert np.all(got[M] == 7.0)
+    info = torch.finfo(torch.float16)
+    bound = sums_error(K) * S
+    bound += info.eps / 2 * (np.abs(ref) + bound) + info.smallest_normal * info.eps
+    err = np.abs(got[:M] - ref)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+# two tokens for each SM and more take other kernels than a few
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("H", [16, 1040, 4096, 4112, 5008, 8192])
+@pytest.mark.parametrize("post,gated,residual", [(True, True, True), (False, False, False),
+                                                 (True, False, True)])
+def test_block_norm_of_many_tokens(apex, H, post, gated, residual, dtype):
+    T = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 4
+    t = TYPES[dtype]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(H)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(t)    # noqa: E731
+    x, pre = rand(T, H), rand(H)
+    r = rand(T, H) if residual else None
+    w = rand(H) if post else None
+    g = rand(T // 4, H) if gated else None
+    offset, alpha = (1.0, 0.5) if post else (0.0, 1.0)
+    kw = dict(residual=r, post_weight=w, gate=g, alpha=alpha, weight_offset=offset, out="both")
+    h, y, codes, scales = apex.block_norm(x, pre, **kw)
+    o = [None if v is None else host(v) for v in (pre, r, w, g)]
+    rh, ry = ob.block_norm(host(x), *o, alpha, 1e-6, offset)
+    # fp32 before the one rounding: a mean of H squares (log2 H + 8 roundings, halved by the root)
+    # and a dozen products, of each of the sum's two terms
+    info, rel = torch.finfo(t), 32 * 2.0 ** -24
+    parts = np.abs(rh - (0 if r is None else o[1])) + (0 if r is None else np.abs(o[1]))
+    half = info.eps / 2 * 1.01
+    low = info.smallest_normal * info.eps
+    assert np.all(np.abs(host(h) - rh) <= half * np.abs(rh) + 4 * rel * parts + low)
+    rms = np.sqrt((rh ** 2).mean(1, keepdims=True))
+    size = np.abs(ry) + np.abs(o[0] + offset) * parts / rms
+    assert np.all(np.abs(host(y) - ry) <= half * np.abs(ry) + 8 * rel * size + low)
+    s = scales.double().cpu().numpy()
+    want = ob.scale_of(np.stack([np.abs(ry[:, i:i + 128]).max(1) for i in range(0, H, 128)], 1))
+    assert np.all(np.abs(s - want) <= 2.0 ** -16 * want)
+    q = ob.rows_values(codes.cpu().numpy(), s)
+    step = np.repeat(s, 128, axis=1)[:, :H] * 2.0 ** -10
+    assert np.all(np.abs(q - ry) <= np.maximum(np.abs(ry) * 2.0 ** -4, step) * 1.001 + 8 * rel * size)
+    # the same rows in a small batch: the sums' order alone is another
+    few = apex.block_norm(x[:4].contiguous(), pre, **{**kw, "residual": None if r is None else r[:4].contiguous(),
+                                                       "gate": None if g is None else g[:1].contiguous()})
+    assert np.all(np.abs(host(few[0]) - host(h)[:4]) <= 2 * half * np.abs(rh[:4]) + 8 * rel * parts[:4] + low)
