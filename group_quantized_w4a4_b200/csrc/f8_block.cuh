@@ -217,12 +217,12 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
 }
 
 // Activations [M][K] (K % 16 == 0) -> E4M3 codes [M][K] and scales [M][G], G = ceil(K / 128).
-// Bound: HBM, 2 bytes in and 1 + 4/128 out per element.  A half-warp owns one (row, group):
-// one 16-byte load a lane, a shuffle maximum, one 8-byte store a lane; UPT groups in flight
-// per half-warp, so that enough loads cover the latency of a large batch.  Measured: 4096 x 8192
-// 33 us (15 at the copy rate; the exact rounding keeps the issue slots 56 % busy), a decode
-// step's 16 x 8192 2.3 us.
-template <int DT, int UPT>
+// Bound: the issue slots for a large batch (the exact rounding; HBM's 2 bytes in and 1 + 4/128 out
+// an element take half as long), latency for a small one.  A half-warp owns one (row, group): one
+// 16-byte load a lane, a shuffle maximum, one 8-byte store a lane.  Measured: 4096 x 8192 29.8 us
+// (bf16 34.7; 15 at the copy rate), a decode step's 16 x 8192 1.7 us.  Two groups in flight a half-warp were
+// slower at every size but one (32.7 us, 2.2; 512 x 8192: 4.9 against 5.1).
+template <int DT>
 __global__ void __launch_bounds__(128) f8_quantize_act_kernel(const void* __restrict__ x, int M,
                                                               int K, int G, int g_shift,
                                                               uint8_t* __restrict__ codes,
@@ -231,34 +231,20 @@ __global__ void __launch_bounds__(128) f8_quantize_act_kernel(const void* __rest
   grid_dep_launch();
   const int hl = threadIdx.x & 15;
   const long long units = (long long)M * G;
-  const long long step = (long long)gridDim.x * 8 * UPT;
+  const long long step = (long long)gridDim.x * 8;
   // every lane of a warp runs the same number of rounds (the shuffles are warp-wide)
-  for (long long u0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5) * 2) * UPT; u0 < units;
-       u0 += step) {
-    float v[UPT][8];
-    int row[UPT], g[UPT];
-    bool in[UPT];
-#pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const long long u = u0 + ((threadIdx.x >> 4) & 1) + 2 * i;
-      const uint32_t w = (uint32_t)(u < units ? u : 0);
-      row[i] = g_shift >= 0 ? (int)(w >> g_shift) : (int)(w / (uint32_t)G);
-      g[i] = (int)w - row[i] * G;
-      in[i] = u < units && g[i] * 128 + hl * 8 < K;
-      if (u >= units) row[i] = -1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-      if (in[i]) load8<DT>(x, (size_t)row[i] * K + g[i] * 128 + hl * 8, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const F8Scale q = f8_scale(half_warp_max(absmax8_bits(v[i])));
-      if (in[i]) {
-        *reinterpret_cast<uint2*>(codes + (size_t)row[i] * K + g[i] * 128 + hl * 8) =
-            f8_codes8<DT == DT_F32>(v[i], q);
-      }
-      if (hl == 0 && row[i] >= 0) scales[(size_t)row[i] * G + g[i]] = q.s;
-    }
+  for (long long u0 = (long long)blockIdx.x * 8 + (threadIdx.x >> 5) * 2; u0 < units; u0 += step) {
+    const long long u = u0 + ((threadIdx.x >> 4) & 1);
+    const uint32_t w = (uint32_t)(u < units ? u : 0);
+    const int row = g_shift >= 0 ? (int)(w >> g_shift) : (int)(w / (uint32_t)G);
+    const int g = (int)w - row * G;
+    const bool in = u < units && g * 128 + hl * 8 < K;
+    const size_t at = (size_t)row * K + g * 128 + hl * 8;
+    float v[8] = {};
+    if (in) load8<DT>(x, at, v);
+    const F8Scale q = f8_scale(half_warp_max(absmax8_bits(v)));
+    if (in) *reinterpret_cast<uint2*>(codes + at) = f8_codes8<DT == DT_F32>(v, q);
+    if (hl == 0 && u < units) scales[(size_t)row * G + g] = q.s;
   }
 }
 

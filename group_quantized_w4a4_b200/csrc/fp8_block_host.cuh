@@ -101,18 +101,12 @@ cudaError_t f8_quantize_t(const void* x, int64_t M, int64_t K, void* codes, void
                           cudaStream_t s) {
   const int G = (int)ceil_div(K, 128);
   const int g_shift = (G & (G - 1)) == 0 ? __builtin_ctz((unsigned)G) : -1;
-  const int64_t units = M * G;
-  const bool many = units >= kQuantBatchMinUnits;
-  const int64_t per_block = 8 * (many ? 2 : 1);
-  int64_t blocks = ceil_div(units, per_block);
+  int64_t blocks = ceil_div(M * G, 8);
   const int64_t cap = (int64_t)dev_info().sms * 32;
   if (blocks > cap) blocks = cap;
-  return many ? launch_pdl(apex::f8_quantize_act_kernel<DT, 2>, (unsigned)blocks, 128, 0, s, x,
-                           (int)M, (int)K, G, g_shift, static_cast<uint8_t*>(codes),
-                           static_cast<float*>(scales))
-              : launch_pdl(apex::f8_quantize_act_kernel<DT, 1>, (unsigned)blocks, 128, 0, s, x,
-                           (int)M, (int)K, G, g_shift, static_cast<uint8_t*>(codes),
-                           static_cast<float*>(scales));
+  return launch_pdl(apex::f8_quantize_act_kernel<DT>, (unsigned)blocks, 128, 0, s, x, (int)M,
+                    (int)K, G, g_shift, static_cast<uint8_t*>(codes),
+                    static_cast<float*>(scales));
 }
 
 apex_status_t check_f8_dims(int64_t M, int64_t N, int64_t K) {
