@@ -434,9 +434,10 @@ apex_status_t apex_pack_weights_fp8_block(const void *w, int32_t dtype, int64_t 
                                           int64_t K, void *codes, void *scales_f32, void *stream);
 
 /*
- * y [M][N] (fp16 / bf16, 2-byte aligned) = sum_g P_g[m,n] * a_scales[m,g] * w_scales[n/128,g],
+ * y [M][N] (fp16 / bf16, 2-byte aligned) = sum_g P_g[m,n] * (a_scales[m,g] * w_scales[n/128,g]),
  * P_g the product over the 128-wide K-group g, everything accumulated in fp32 and rounded once.
- * Any finite, infinite or NaN codes and scales are multiplied as they are.
+ * Any finite, infinite or NaN codes and scales are multiplied as they are, the two scales first:
+ * scales whose product leaves fp32's range give infinities, NaNs or zeros.
  */
 apex_status_t apex_gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void *a_codes,
                                   const void *a_scales, const void *w_codes,
