@@ -30,9 +30,11 @@
 // there, every fourth group waited 1,100 cycles for them.
 //
 // Bound: the partials' way out of tensor memory and the fma on each; the tensor pipe is 59 %
-// busy.  Measured: 4096 x 8192 x 8192 244 us (2.25 PFLOP/s; a library product with one scale a
-// tensor 190), with the quantizer 277, 327 in an unbroken loop under the power cap.  CTA pairs
-// with 256 x 256 tiles took the same time and left more of a ragged tile empty.
+// busy.  Measured: 4096 x 8192 x 8192 248 us (2.2 PFLOP/s; a library product with one scale a
+// tensor 190), one call with the quantizer and a cold L2 286, 328 in an unbroken loop under the
+// power cap.  CTA pairs with 256 x 256 tiles took the same time and left more of a ragged tile
+// empty.  Experts, 32768 rows through 64 of 2048 x 1024: UP 206 us; DOWN 136 (116 with 16-bit rows:
+// 134 MB less to write, and no buffers to wait for).
 #pragma once
 #include <cuda.h>
 #include <stdint.h>

@@ -17,8 +17,8 @@
 // early: the launch follows the activations' quantizer (or FB_UP) of the same call, which
 // lets its dependents start only after everything before it has finished.  Weights, offsets
 // and order are then complete, and the first stages' weights are fetched while it still runs.
-// Measured: 8192 x 8192, 1 and 16 tokens, with the quantizer: 16.8 and 17.9 us (67 MB: 10.3 us at
-// the copy rate); 64 experts of 2048 x 1024, 16 tokens, the whole MLP: 66 us (297 MB: 45 us).
+// Measured: 8192 x 8192, 1 and 16 tokens, with the quantizer: 16.8 and 18.0 us (67 MB: 10.3 us at
+// the copy rate); 64 experts of 2048 x 1024, 16 tokens, the whole MLP: 68 us (297 MB: 45 us).
 // Roles (192 threads): warp 0 TMA, warp 1 MMA, warps 2..5 epilogue (lanes 32 * (warp % 4)..).
 #pragma once
 #include <cuda.h>
