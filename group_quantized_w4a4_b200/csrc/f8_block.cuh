@@ -219,9 +219,9 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
 // Activations [M][K] (K % 16 == 0) -> E4M3 codes [M][K] and scales [M][G], G = ceil(K / 128).
 // Bound: the issue slots for a large batch (the exact rounding; HBM's 2 bytes in and 1 + 4/128 out
 // an element take half as long), latency for a small one.  A half-warp owns one (row, group): one
-// 16-byte load a lane, a shuffle maximum, one 8-byte store a lane.  Measured: 4096 x 8192 29.8 us
-// (bf16 34.7; 15 at the copy rate), a decode step's 16 x 8192 1.7 us.  Two groups in flight a half-warp were
-// slower at every size but one (32.7 us, 2.2; 512 x 8192: 4.9 against 5.1).
+// 16-byte load a lane, a shuffle maximum, one 8-byte store a lane.  Measured: 4096 x 8192 29.5 us
+// (bf16 34.7; 15 at the copy rate), a decode step's 16 x 8192 1.7 us.  Two groups in flight a
+// half-warp were slower at every size but one (32.8 us, 2.2; 512 x 8192: 4.9 against 5.1).
 template <int DT>
 __global__ void __launch_bounds__(128) f8_quantize_act_kernel(const void* __restrict__ x, int M,
                                                               int K, int G, int g_shift,
